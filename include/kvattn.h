@@ -52,6 +52,7 @@
 #ifndef KVATTN_H
 #define KVATTN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -348,6 +349,161 @@ int kvattn_mla_rope_append_fp8(uint16_t *q_rope, const uint16_t *latent_new, con
                                int max_seq_len, int batch, int n_heads, int latent_dim, int rope_dim,
                                float rope_base, int interleaved, float latent_scale, float rope_scale,
                                void *stream);
+
+/*
+ * A paged E4M3 cache with one scale per cached row.
+ *
+ * A row is one token's key (or value) of one KV head.  Its scale comes from the row itself,
+ *     scale = a / 448,  a = max(max_i |y_i|, 2^-55),   code_i = E4M3(y_i * (448 / a))
+ * (nearest, ties to even, saturated; a is at most the largest finite float, NaN elements are
+ * passed over in a and become the NaN code), and the cached value is code_i * scale.  So a
+ * cache is quantised as it is written, without calibrated tensor scales, and an outlier token
+ * costs no other token precision.  ("Attention variants: MQA, GQA, and MLA", section "Against
+ * the real libraries", names quantised caches and paged caches; the pages give no format.)
+ *   k_pages, v_pages    device E4M3 codes [num_pages, n_kv_heads, page_size, head_dim]
+ *   k_scales, v_scales  device fp32 [num_pages, n_kv_heads, page_size]
+ *   a slot              page * page_size + row
+ *   num_pages * n_kv_heads * page_size < 2^31
+ *
+ * kvattn_rope_append_rowscale writes n_tokens new tokens of any sequences (one each in a
+ * decode step, a whole prompt in a prefill) and rotates their queries and keys:
+ *   q          device bf16 [n_tokens, n_q_heads, head_dim], or NULL (then q_out is NULL and
+ *              n_q_heads 0); the rotated queries go to q_out (same shape), which may be q itself
+ *              with the same stride (in place)
+ *   k_new, v_new  device bf16 [n_tokens, n_kv_heads, head_dim]
+ *   *_stride   elements from one token to the next (a multiple of 8, at least the token's
+ *              own elements): slices of a fused projection are read in place
+ *   positions  device int32 [n_tokens]: the angle's position; NULL allowed without rotation
+ *   slots      device int64 [n_tokens]: where each token goes; a slot outside the pool (such
+ *              as -1) is not written (its query is still rotated).  Slots must be distinct:
+ *              a slot given twice holds a mixture of its tokens afterwards.
+ *   rope_base  as for kvattn_rope_append; 0: no rotation (q is copied to q_out)
+ *   head_dim   a multiple of 16, <= 256
+ * The angle is formed in fp64 and the scales and codes from the fp32 rotated values.
+ * n_tokens may be 0 (nothing is launched).  q_out, the pools and the scales must not overlap
+ * each other or the inputs (but for q in place).
+ */
+int kvattn_rope_append_rowscale(const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new,
+                                const int32_t *positions, const int64_t *slots, uint16_t *q_out, uint8_t *k_pages,
+                                uint8_t *v_pages, float *k_scales, float *v_scales, int n_tokens, int n_q_heads,
+                                int n_kv_heads, int head_dim, int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
+                                int64_t v_stride, int num_pages, int page_size, float rope_base, int interleaved,
+                                void *stream);
+
+/*
+ * Reads rows of a row-scaled cache back to bf16 (code * scale, rounded once):
+ *   slots         device int64 [n_tokens]; a slot outside the pool gives a row of zeros
+ *   k_out, v_out  device bf16 [n_kv_heads, n_tokens, head_dim], heads k_head_stride /
+ *                 v_head_stride elements apart (a multiple of 8): the layout
+ *                 kvattn_gqa_decode_prefix takes its prefix in, and a part of a longer one
+ * head_dim a multiple of 16, <= 256.  n_tokens may be 0.
+ */
+int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales, const float *v_scales,
+                           const int64_t *slots, uint16_t *k_out, uint16_t *v_out, int n_tokens, int n_kv_heads,
+                           int head_dim, int64_t k_head_stride, int64_t v_head_stride, int num_pages, int page_size,
+                           void *stream);
+
+/*
+ * Decode over a row-scaled cache, the form of kvattn_gqa_decode_fp8 (several new tokens and a
+ * window included) with a scale per row: s_t = scale * k_scale_t (q . kcode_t),
+ * out = sum_t softmax(s)_t v_scale_t vcode_t.
+ *   q            device bf16 [batch, q_len, n_q_heads, head_dim]
+ *   block_table  device int32 [batch, max_pages_per_seq] as for kvattn_gqa_decode_paged, or NULL:
+ *                a contiguous cache, one page a sequence (num_pages = batch,
+ *                max_pages_per_seq = 1, page_size = the capacity)
+ *   out          device bf16 [batch, q_len, n_q_heads, head_dim], rounded once: the type the
+ *                output projection reads, and what the weights' two E4M3 parts (~8 significant
+ *                bits) support;  lse fp32 [batch, q_len, n_q_heads]
+ * head_dim 128, n_q_heads / n_kv_heads <= 64, page_size a multiple of 128 (paged); batch *
+ * q_len <= 4096.  Scales from 2^-60 to 2^60 keep full precision.  Codes and scales past a
+ * sequence's length are never read into a result; everything else as for
+ * kvattn_gqa_decode_fp8.
+ */
+int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales,
+                               const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, int num_pages,
+                               int page_size, int max_pages_per_seq, int batch, int q_len, int n_q_heads, int n_kv_heads,
+                               int head_dim, float scale, int window, uint16_t *out, float *lse, void *stream);
+
+/*
+ * Decode for a batch whose sequences share a prefix: every new token attends to the same
+ * prefix tokens and then, causally, to its own sequence's cache.  The prefix is read once for
+ * the whole batch (a matrix product of all sequences' query rows), not once per sequence.
+ *   q          device bf16 [batch, q_len, n_q_heads, head_dim], the newest tokens, oldest first
+ *   k_prefix, v_prefix  device bf16 [n_kv_heads, max_prefix_len, head_dim]
+ *   prefix_len device int32 [1], 0..max_prefix_len (clamped): tokens of the shared prefix
+ *   k_cache, v_cache  device bf16 [batch, n_kv_heads, max_seq_len, head_dim]: each sequence's
+ *              own tokens, which follow the prefix
+ *   seq_lens   device int32 [batch]: own tokens, the q_len new ones included, 0..max_seq_len
+ *              (clamped).  Query i of sequence b attends to the whole prefix and to own
+ *              positions t <= seq_lens[b] - q_len + i (none where that is negative).
+ *   out        device bf16 [batch, q_len, n_q_heads, head_dim];  lse fp32 [batch, q_len,
+ *              n_q_heads] over prefix and own tokens.  A query with nothing to attend to
+ *              (prefix_len 0 and no own token) gets out = 0 and lse = -inf.
+ *   workspace  device, 16-byte aligned, at least the bytes that
+ *              kvattn_gqa_decode_prefix_workspace gives for the same sizes: scratch of this one
+ *              call, never kept.  Calls that may run at the same time (other streams, other
+ *              captured graphs) need a workspace each; the library allocates nothing.
+ *   head_dim 64 or 128; (n_q_heads / n_kv_heads) * q_len <= 128; batch * q_len <= 4096;
+ *   batch * n_kv_heads * max_seq_len and n_kv_heads * max_prefix_len < 2^31.
+ * The softmax weights enter the value products as bf16; sums and outputs accumulate in fp32.
+ * Rows at or past prefix_len and seq_lens[b] are never read into a result.  With q_len > 1 a
+ * new token's cached value has to be finite also for the older new tokens, which give it
+ * weight zero.
+ *
+ * kvattn_gqa_decode_prefix_paged takes prefix and own tokens from one page pool:
+ *   k_pages, v_pages  device bf16 [num_pages, n_kv_heads, page_size, head_dim], page_size a
+ *              multiple of 128
+ *   prefix_table  device int32 [max_prefix_pages], the prefix's pages;  block_table device
+ *              int32 [batch, max_pages_per_seq], each sequence's own pages (after the prefix).
+ *              A page outside the pool reads as zeros.
+ * Its workspace is that of max_prefix_len = max_prefix_pages * page_size and max_seq_len =
+ * max_pages_per_seq * page_size.
+ */
+int kvattn_gqa_decode_prefix_workspace(int max_prefix_len, int max_seq_len, int batch, int q_len, int n_q_heads,
+                                       int n_kv_heads, int head_dim, size_t *bytes);
+int kvattn_gqa_decode_prefix(const uint16_t *q, const uint16_t *k_prefix, const uint16_t *v_prefix,
+                             const int32_t *prefix_len, int max_prefix_len, const uint16_t *k_cache,
+                             const uint16_t *v_cache, const int32_t *seq_lens, int max_seq_len, int batch, int q_len,
+                             int n_q_heads, int n_kv_heads, int head_dim, float scale, uint16_t *out, float *lse,
+                             void *workspace, size_t workspace_bytes, void *stream);
+int kvattn_gqa_decode_prefix_paged(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                                   const int32_t *prefix_table, const int32_t *prefix_len, int max_prefix_pages,
+                                   const int32_t *block_table, const int32_t *seq_lens, int num_pages, int page_size,
+                                   int max_pages_per_seq, int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                   int head_dim, float scale, uint16_t *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling): which of a sequence's drafts the
+ * target model's probabilities accept, and the token that follows them, from random numbers
+ * of the caller.  The step after kvattn_gqa_decode_multi (or a prefix / row-scaled decode)
+ * has scored the drafts.
+ * Draft i (token x, target probabilities p_i, draft probabilities q_i) is accepted while
+ * u_accept[b, i] * q_i(x) < p_i(x).  At the first refusal n the next token is drawn from
+ * max(p_n - q_n, 0), normalised (from p_n where that is zero everywhere); with all of the
+ * sequence's drafts accepted, from p_n with n = draft_lens[b].  The draw is the first token
+ * v with sum_{w <= v} r_w > u_sample[b] * sum_w r_w; products and sums are taken in 64 bits.
+ *   target_probs  device [batch, n_drafts + 1, vocab], fp32 (bf16 == 0) or bf16, vocabulary
+ *                 contiguous, the other axes target_batch_stride / target_pos_stride elements
+ *   draft_probs   device [batch, n_drafts, vocab] of the same type with its strides, or NULL:
+ *                 point drafts (probability 1 at the drafted token, as a greedy or a lookup
+ *                 draft has)
+ *   draft_tokens  device int32 [batch, n_drafts]; one outside [0, vocab) is refused
+ *   draft_lens    device int32 [batch], drafts of each sequence (clamped to 0..n_drafts), or
+ *                 NULL: n_drafts each
+ *   u_accept, u_sample  device fp32 [batch, n_drafts], [batch], uniform in [0, 1)
+ *   accepted      device int32 [batch]: n
+ *   tokens        device int32 [batch, n_drafts + 1]: the accepted drafts, the drawn token, -1
+ * n_drafts may be 0 (then a plain draw from target_probs; draft_tokens and u_accept may be
+ * NULL); n_drafts <= 1024, batch <= 4096, vocab <= 2^28.  Probabilities need not sum to one;
+ * negative and NaN entries are never drawn; a row without a positive entry gives token -1.
+ * Rows whose strides and pointers are multiples of 16 bytes are read in vectors, others by
+ * element.
+ */
+int kvattn_verify_drafts(const void *target_probs, const void *draft_probs, const int32_t *draft_tokens,
+                         const int32_t *draft_lens, const float *u_accept, const float *u_sample, int32_t *accepted,
+                         int32_t *tokens, int batch, int n_drafts, int vocab, int bf16, int64_t target_batch_stride,
+                         int64_t target_pos_stride, int64_t draft_batch_stride, int64_t draft_pos_stride, void *stream);
 
 /* Human-readable name of a kvattn_status value (static string, never NULL). */
 const char *kvattn_status_string(int status);

@@ -87,6 +87,21 @@ _SIGNATURES = {
                                                ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_float,
                                                ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvattn_rope_append_rowscale": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_int] * 4 + [ctypes.c_int64] * 4 +
+                                    [ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_void_p]),
+    "kvattn_gather_rowscale": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 3 + [ctypes.c_int64] * 2 +
+                               [ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "kvattn_gqa_decode_rowscale": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 8 +
+                                   [ctypes.c_float, ctypes.c_int] + [ctypes.c_void_p] * 3),
+    "kvattn_gqa_decode_prefix_workspace": (ctypes.c_int, [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "kvattn_gqa_decode_prefix": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] + [ctypes.c_void_p] * 3 +
+                                 [ctypes.c_int] * 6 + [ctypes.c_float] + [ctypes.c_void_p] * 3 +
+                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "kvattn_gqa_decode_prefix_paged": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] + [ctypes.c_void_p] * 2 +
+                                       [ctypes.c_int] * 8 + [ctypes.c_float] + [ctypes.c_void_p] * 3 +
+                                       [ctypes.c_size_t, ctypes.c_void_p]),
+    "kvattn_verify_drafts": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int] * 4 + [ctypes.c_int64] * 4 +
+                             [ctypes.c_void_p]),
     "kvattn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kvattn_last_error_detail": (ctypes.c_char_p, []),
     "kvattn_version": (ctypes.c_int, []),
@@ -619,3 +634,322 @@ def kvattn_gqa_decode_multi(q, k_cache, v_cache, seq_lens, scale, window=0, out=
     if st != KVATTN_OK:
         raise KvattnError(st, "kvattn_gqa_decode_multi")
     return out, lse
+
+
+class _On:
+    """Runs a call on its stream and on its tensors' device: what it allocates belongs to that
+    stream.  The stream is the given one, else the device's current one."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self._device = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self._stream = torch.cuda.stream(stream) if stream is not None else None
+        self._handle_of = torch.cuda.current_stream
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return ctypes.c_void_p(self._handle_of().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def _check_on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _check_rows(t, name, shape):
+    """bf16 [N, heads, d], each token's heads dense, tokens any stride apart; returns the stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, h, d = shape
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name}'s heads must be dense within a token")
+    return s[0] if n > 1 else h * d
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kvattn_rope_append_rowscale(q, k_new, v_new, positions, slots, k_pages, v_pages, k_scales, v_scales,
+                                rope_base=10000.0, interleaved=False, q_out=None, stream=None):
+    """Rotary embedding of N new tokens and their write into a row-scaled E4M3 page pool
+    (include/kvattn.h, kvattn_rope_append_rowscale): q [N, n_q, d] (or None), k_new / v_new
+    [N, n_kv, d] bf16 (token-strided views allowed), positions [N] int32, slots [N] int64;
+    k_pages / v_pages [P, n_kv, page_size, d] float8_e4m3fn (or uint8), k_scales / v_scales
+    [P, n_kv, page_size] fp32.  rope_base 0: no rotation (positions may be None).  q is rotated
+    in place unless q_out is given; returns the rotated queries (None without q)."""
+    import torch
+    N, n_kv, d = k_new.shape
+    P, S = k_pages.shape[0], k_pages.shape[2]
+    dev = k_new.device
+    ks = _check_rows(k_new, "k_new", (N, n_kv, d))
+    vs = _check_rows(v_new, "v_new", (N, n_kv, d))
+    n_q, qs, os_ = 0, 0, 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        n_q = q.shape[1]
+        q_out = q if q_out is None else q_out
+        qs = _check_rows(q, "q", (N, n_q, d))
+        os_ = _check_rows(q_out, "q_out", (N, n_q, d))
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (N,))
+    _check(slots, "slots", torch.int64, (N,))
+    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
+    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
+    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
+    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
+    _check_on(dev, q=q, q_out=q_out, v_new=v_new, positions=positions, slots=slots, k_pages=k_pages, v_pages=v_pages,
+              k_scales=k_scales, v_scales=v_scales)
+    if N == 0:
+        return q_out
+    with _On(dev, stream) as st:
+        rc = lib().kvattn_rope_append_rowscale(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), _ptr(positions),
+                                               slots.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
+                                               k_scales.data_ptr(), v_scales.data_ptr(), N, n_q, n_kv, d, qs, os_, ks,
+                                               vs, P, S, float(rope_base), int(bool(interleaved)), st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_rope_append_rowscale")
+    return q_out
+
+
+def kvattn_gather_rowscale(k_pages, v_pages, k_scales, v_scales, slots, k_out=None, v_out=None, stream=None):
+    """Rows of a row-scaled page pool read back to bf16 (include/kvattn.h,
+    kvattn_gather_rowscale): slots [N] int64.  Returns (k, v) [n_kv, N, d] bf16; k_out / v_out
+    may be given, also as parts k_prefix[:, a:a + N] of longer buffers."""
+    import torch
+    P, n_kv, S, d = k_pages.shape
+    N = slots.shape[0]
+    dev = k_pages.device
+    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
+    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
+    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
+    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
+    _check(slots, "slots", torch.int64, (N,))
+    with _On(dev, stream) as st:
+        if k_out is None:
+            k_out = torch.empty((n_kv, N, d), dtype=torch.bfloat16, device=dev)
+        if v_out is None:
+            v_out = torch.empty((n_kv, N, d), dtype=torch.bfloat16, device=dev)
+        kh = _check_rows(k_out, "k_out", (n_kv, N, d))
+        vh = _check_rows(v_out, "v_out", (n_kv, N, d))
+        _check_on(dev, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, slots=slots, k_out=k_out, v_out=v_out)
+        if N == 0:
+            return k_out, v_out
+        rc = lib().kvattn_gather_rowscale(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                          v_scales.data_ptr(), slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), N,
+                                          n_kv, d, kh, vh, P, S, st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_gather_rowscale")
+    return k_out, v_out
+
+
+def _outputs(q, out, lse):
+    """bf16 out like q and fp32 lse without its last axis, allocated where not given."""
+    import torch
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    _check(out, "out", torch.bfloat16, q.shape)
+    _check(lse, "lse", torch.float32, q.shape[:-1])
+    return out, lse
+
+
+def _q_shape(q):
+    """(B, L, n_q, d) of q [B, n_q, d] or [B, L, n_q, d]."""
+    return (q.shape[0], 1, q.shape[1], q.shape[2]) if q.dim() == 3 else tuple(q.shape)
+
+
+def kvattn_gqa_decode_rowscale(q, k_pages, v_pages, k_scales, v_scales, seq_lens, scale, block_table=None, window=0,
+                               out=None, lse=None, stream=None):
+    """Decode over a row-scaled E4M3 cache (include/kvattn.h, kvattn_gqa_decode_rowscale): q
+    [B, n_q, 128] (one new token) or [B, L, n_q, 128] bf16; k_pages / v_pages [P, n_kv,
+    page_size, 128] codes with k_scales / v_scales [P, n_kv, page_size] fp32 and block_table
+    [B, max_pages] int32, or without it [B, n_kv, T, 128] and [B, n_kv, T].  Returns (out bf16
+    like q, lse fp32)."""
+    import torch
+    B, L, n_q, d = _q_shape(q)
+    P, n_kv, S, _ = k_pages.shape
+    M = block_table.shape[1] if block_table is not None else 1
+    dev = q.device
+    _check(q, "q", torch.bfloat16)
+    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
+    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
+    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
+    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    if block_table is not None:
+        _check(block_table, "block_table", torch.int32, (B, M))
+    with _On(dev, stream) as st:
+        out, lse = _outputs(q, out, lse)
+        _check_on(dev, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, seq_lens=seq_lens,
+                  block_table=block_table, out=out, lse=lse)
+        rc = lib().kvattn_gqa_decode_rowscale(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                              v_scales.data_ptr(), _ptr(block_table), seq_lens.data_ptr(), P, S, M, B, L,
+                                              n_q, n_kv, d, float(scale), int(window), out.data_ptr(), lse.data_ptr(), st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_gqa_decode_rowscale")
+    return out, lse
+
+
+def kvattn_gqa_decode_prefix_workspace(max_prefix_len, max_seq_len, batch, q_len, n_q_heads, n_kv_heads, head_dim):
+    """Bytes of workspace a shared-prefix decode of these sizes needs on the current device."""
+    n = ctypes.c_size_t(0)
+    rc = lib().kvattn_gqa_decode_prefix_workspace(max_prefix_len, max_seq_len, batch, q_len, n_q_heads, n_kv_heads,
+                                                  head_dim, ctypes.byref(n))
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_gqa_decode_prefix_workspace")
+    return int(n.value)
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, or one of torch's allocator for this call alone (stream-ordered;
+    inside a graph capture it belongs to the graph)."""
+    import torch
+    if workspace is None:
+        return torch.empty((need,), dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", torch.uint8)
+    if workspace.dim() != 1 or workspace.numel() < need:
+        raise ValueError(f"workspace must be a vector of at least {need} bytes")
+    return workspace
+
+
+def kvattn_gqa_decode_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, scale, out=None, lse=None,
+                             workspace=None, stream=None):
+    """Decode for a batch that shares a prefix (include/kvattn.h, kvattn_gqa_decode_prefix): q
+    [B, n_q, d] or [B, L, n_q, d] bf16, k_prefix / v_prefix [n_kv, P, d] bf16 with prefix_len [1]
+    int32, k_cache / v_cache [B, n_kv, T, d] bf16 with seq_lens [B] int32.  Returns (out bf16 like
+    q, lse fp32).  workspace: uint8, kvattn_gqa_decode_prefix_workspace bytes."""
+    import torch
+    B, L, n_q, d = _q_shape(q)
+    n_kv, P, _ = k_prefix.shape
+    T = k_cache.shape[2]
+    dev = q.device
+    _check(q, "q", torch.bfloat16)
+    _check(k_prefix, "k_prefix", torch.bfloat16, (n_kv, P, d))
+    _check(v_prefix, "v_prefix", torch.bfloat16, (n_kv, P, d))
+    _check(prefix_len, "prefix_len", torch.int32, (1,))
+    _check(k_cache, "k_cache", torch.bfloat16, (B, n_kv, T, d))
+    _check(v_cache, "v_cache", torch.bfloat16, (B, n_kv, T, d))
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    with _On(dev, stream) as st:
+        out, lse = _outputs(q, out, lse)
+        ws = _workspace(workspace, kvattn_gqa_decode_prefix_workspace(P, T, B, L, n_q, n_kv, d), dev)
+        _check_on(dev, k_prefix=k_prefix, v_prefix=v_prefix, prefix_len=prefix_len, k_cache=k_cache, v_cache=v_cache,
+                  seq_lens=seq_lens, out=out, lse=lse, workspace=ws)
+        rc = lib().kvattn_gqa_decode_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), prefix_len.data_ptr(),
+                                            P, k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(), T, B, L, n_q,
+                                            n_kv, d, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                            ws.numel(), st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_gqa_decode_prefix")
+    return out, lse
+
+
+def kvattn_gqa_decode_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, scale, out=None,
+                                   lse=None, workspace=None, stream=None):
+    """kvattn_gqa_decode_prefix with prefix and own tokens in one page pool (include/kvattn.h,
+    kvattn_gqa_decode_prefix_paged): k_pages / v_pages [num_pages, n_kv, page_size, d] bf16,
+    prefix_table [max_prefix_pages] and block_table [B, max_pages] int32."""
+    import torch
+    B, L, n_q, d = _q_shape(q)
+    N, n_kv, S, _ = k_pages.shape
+    PM, M = prefix_table.shape[0], block_table.shape[1]
+    dev = q.device
+    _check(q, "q", torch.bfloat16)
+    _check(k_pages, "k_pages", torch.bfloat16, (N, n_kv, S, d))
+    _check(v_pages, "v_pages", torch.bfloat16, (N, n_kv, S, d))
+    _check(prefix_table, "prefix_table", torch.int32, (PM,))
+    _check(prefix_len, "prefix_len", torch.int32, (1,))
+    _check(block_table, "block_table", torch.int32, (B, M))
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    with _On(dev, stream) as st:
+        out, lse = _outputs(q, out, lse)
+        ws = _workspace(workspace, kvattn_gqa_decode_prefix_workspace(PM * S, M * S, B, L, n_q, n_kv, d), dev)
+        _check_on(dev, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table, prefix_len=prefix_len,
+                  block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=ws)
+        rc = lib().kvattn_gqa_decode_prefix_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                                  prefix_table.data_ptr(), prefix_len.data_ptr(), PM,
+                                                  block_table.data_ptr(), seq_lens.data_ptr(), N, S, M, B, L, n_q, n_kv,
+                                                  d, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                                  ws.numel(), st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_gqa_decode_prefix_paged")
+    return out, lse
+
+
+def _check_probs(t, name, dtype, shape):
+    """Probabilities [B, L, V], the vocabulary contiguous; returns the other axes' strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s vocabulary axis must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, draft_lens=None, accepted=None,
+                         tokens=None, stream=None):
+    """Verification of drafted tokens (include/kvattn.h, kvattn_verify_drafts): target_probs
+    [B, L + 1, V] fp32 or bf16, draft_probs [B, L, V] of the same type (None: point drafts),
+    draft_tokens [B, L] int32, u_accept [B, L] and u_sample [B] fp32, draft_lens [B] int32 or
+    None.  Rows may be strided (a padded vocabulary).  Returns (accepted [B], tokens [B, L + 1])
+    int32."""
+    import torch
+    B, L1, V = target_probs.shape
+    L = L1 - 1
+    dtype, dev = target_probs.dtype, target_probs.device
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target_probs must be float32 or bfloat16, got {dtype}")
+    tb, tl = _check_probs(target_probs, "target_probs", dtype, (B, L1, V))
+    db, dl = _check_probs(draft_probs, "draft_probs", dtype, (B, L, V)) if draft_probs is not None else (0, 0)
+    _check(draft_tokens, "draft_tokens", torch.int32, (B, L))
+    _check(u_accept, "u_accept", torch.float32, (B, L))
+    _check(u_sample, "u_sample", torch.float32, (B,))
+    if draft_lens is not None:
+        _check(draft_lens, "draft_lens", torch.int32, (B,))
+    with _On(dev, stream) as st:
+        if accepted is None:
+            accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        if tokens is None:
+            tokens = torch.empty((B, L1), dtype=torch.int32, device=dev)
+        _check(accepted, "accepted", torch.int32, (B,))
+        _check(tokens, "tokens", torch.int32, (B, L1))
+        _check_on(dev, draft_probs=draft_probs, draft_tokens=draft_tokens, u_accept=u_accept, u_sample=u_sample,
+                  draft_lens=draft_lens, accepted=accepted, tokens=tokens)
+        rc = lib().kvattn_verify_drafts(target_probs.data_ptr(), _ptr(draft_probs), draft_tokens.data_ptr(),
+                                        _ptr(draft_lens), u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(),
+                                        tokens.data_ptr(), B, L, V, int(dtype == torch.bfloat16), tb, tl, db, dl, st)
+    if rc != KVATTN_OK:
+        raise KvattnError(rc, "kvattn_verify_drafts")
+    return accepted, tokens

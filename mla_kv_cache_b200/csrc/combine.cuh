@@ -19,6 +19,7 @@
 #pragma once
 #include "common.cuh"
 #include "schedule.cuh"
+#include "window.cuh"
 
 namespace kvattn {
 
@@ -26,7 +27,7 @@ struct CombineParams {
     const int32_t *seq_lens;
     const float *ws_lse;   // [workers, 2, heads_per_unit]
     const float *ws_o;     // [workers, 2, heads_per_unit, D]
-    float *out;            // [B, n_q, D]
+    float *out;            // [B, n_q, D] (bf16 when OUT16)
     float *lse;            // [B, n_q]
     int B, n_q;
     int units_per_seq;     // U
@@ -40,11 +41,13 @@ struct CombineParams {
     int min_tiles;         // the decode kernel's minimum tiles per worker
     int q_len;             // new tokens per sequence (rows of a unit: q_len x g)
     int window;            // sliding window (0: none)
+    int start_align;       // windowed ranges start at a multiple of this (0: anywhere)
     int unit_split;        // the decode kernel cuts equal units into parts (unit_part_tiles)
 };
 
 // D columns, D / 32 floats per lane; NW warps share the partials of one output row.
-template <int D, int NW>
+// OUT16: the output is bf16, rounded once from the fp32 merge.
+template <int D, int NW, bool OUT16 = false>
 __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p) {
     constexpr int kCombineWarps = NW;
     constexpr int VEC = D / 32;
@@ -67,11 +70,11 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
 
     // ---- the work split, from seq_lens (an input: readable before the decode grid ends)
     const int l0 = clamp_len(__ldg(p.seq_lens), p.T_max);
-    const int t0 = tiles_of(l0 - active_start(l0, p.q_len, p.window), p.tile);
+    const int t0 = tiles_of(l0 - active_start_on(p.start_align, l0, p.q_len, p.window), p.tile);
     int before = 0, all = 0, same = 1;
     for (int x = threadIdx.x; x < p.B; x += blockDim.x) {
         const int lx = clamp_len(__ldg(p.seq_lens + x), p.T_max);
-        const int t = tiles_of(lx - active_start(lx, p.q_len, p.window), p.tile);
+        const int t = tiles_of(lx - active_start_on(p.start_align, lx, p.q_len, p.window), p.tile);
         all += t;
         same &= t == t0;
         if (x < b) before += t;
@@ -90,11 +93,16 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
 #pragma unroll
     for (int w = 0; w < kCombineWarps; ++w) { before += s_sum[0][w]; all += s_sum[1][w]; same &= s_sum[2][w]; }
     const int len_b = clamp_len(__ldg(p.seq_lens + b), p.T_max);
-    const int n_tiles = tiles_of(len_b - active_start(len_b, p.q_len, p.window), p.tile);
+    const int n_tiles = tiles_of(len_b - active_start_on(p.start_align, len_b, p.q_len, p.window), p.tile);
     const long long W = tiles_per_worker((long long)all * p.units_per_seq, p.workers, p.min_tiles);
     if (n_tiles == 0) {
         // nothing of this unit was touched by the decode kernel
-        for (int c = threadIdx.x; c < D; c += blockDim.x) p.out[gh * D + c] = 0.f;
+        for (int c = threadIdx.x; c < D; c += blockDim.x) {
+            if constexpr (OUT16)
+                reinterpret_cast<__nv_bfloat16 *>(p.out)[gh * D + c] = __float2bfloat16_rn(0.f);
+            else
+                p.out[gh * D + c] = 0.f;
+        }
         if (threadIdx.x == 0) p.lse[gh] = -INFINITY;
         return;
     }
@@ -178,7 +186,12 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
     // start): out 0, lse -inf
     const float inv = tot > 0.f ? 1.f / tot : 0.f;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) p.out[gh * D + col + v] = res[v] * inv;
+    for (int v = 0; v < VEC; ++v) {
+        if constexpr (OUT16)
+            reinterpret_cast<__nv_bfloat16 *>(p.out)[gh * D + col + v] = __float2bfloat16_rn(res[v] * inv);
+        else
+            p.out[gh * D + col + v] = res[v] * inv;
+    }
     if (lane == 0) p.lse[gh] = tot > 0.f ? M + __logf(tot) : -INFINITY;
 }
 

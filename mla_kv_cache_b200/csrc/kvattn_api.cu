@@ -14,7 +14,10 @@
 #include "gqa_decode.cuh"
 #include "gqa_tc_decode.cuh"
 #include "mla_decode.cuh"
+#include "prefix_decode.cuh"
 #include "rope_append.cuh"
+#include "rowscale.cuh"
+#include "verify.cuh"
 
 using namespace kvattn;
 
@@ -252,9 +255,9 @@ int make_map_view(CUtensorMap *map, const void *base, int rank, const uint64_t *
 }
 
 // 4-D bf16 tensor [dim3][dim2][dim1][dim0] (dim0 fastest, densely packed), box
-// {box0, box1, box2, 1}.  Not cached (used once per call).
+// {box0, box1, box2, box3}.  Not cached (used once per call).
 int make_map_4d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2, uint64_t dim3,
-                uint32_t box0, uint32_t box1, uint32_t box2, CUtensorMapSwizzle swz) {
+                uint32_t box0, uint32_t box1, uint32_t box2, uint32_t box3, CUtensorMapSwizzle swz) {
     auto fn = encode_fn();
     if (!fn) {
         snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled unavailable");
@@ -262,7 +265,7 @@ int make_map_4d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1
     }
     cuuint64_t dims[4] = {dim0, dim1, dim2, dim3};
     cuuint64_t strides[3] = {dim0 * 2, dim0 * dim1 * 2, dim0 * dim1 * dim2 * 2};
-    cuuint32_t box[4] = {box0, box1, box2, 1};
+    cuuint32_t box[4] = {box0, box1, box2, box3};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -296,15 +299,15 @@ cudaError_t set_smem_limit(const void *kern, DeviceState *dev, int smem) {
 // Kernels this library has launched from the calling thread (kvattn_kernel_launches).
 thread_local unsigned long long t_launches = 0;
 
-template <int D>
+template <int D, bool OUT16 = false>
 cudaError_t launch_combine_d(cudaLaunchConfig_t &cfg, const CombineParams &cp, int warps) {
     cfg.blockDim = dim3(warps * 32, 1, 1);
     cudaError_t e;
     switch (warps) {
-        case 1: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 1>, cp); break;
-        case 2: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 2>, cp); break;
-        case 4: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 4>, cp); break;
-        default: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 8>, cp); break;
+        case 1: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 1, OUT16>, cp); break;
+        case 2: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 2, OUT16>, cp); break;
+        case 4: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 4, OUT16>, cp); break;
+        default: e = cudaLaunchKernelEx(&cfg, combine_kernel<D, 8, OUT16>, cp); break;
     }
     if (e == cudaSuccess) ++t_launches;
     return e;
@@ -321,7 +324,8 @@ int combine_warps(long long tiles_per_unit_max, long long total_tiles_max, int w
     return 8;
 }
 
-int launch_combine(int D, const CombineParams &cp, int units, int rows, cudaStream_t stream, int warps) {
+int launch_combine(int D, const CombineParams &cp, int units, int rows, cudaStream_t stream, int warps,
+                   bool out16 = false) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -335,7 +339,7 @@ int launch_combine(int D, const CombineParams &cp, int units, int rows, cudaStre
     if (D == 64)
         e = launch_combine_d<64>(cfg, cp, warps);
     else if (D == 128)
-        e = launch_combine_d<128>(cfg, cp, warps);
+        e = out16 ? launch_combine_d<128, true>(cfg, cp, warps) : launch_combine_d<128>(cfg, cp, warps);
     else
         e = launch_combine_d<512>(cfg, cp, warps);
     if (e != cudaSuccess) return fail_cuda(e, "combine launch");
@@ -477,6 +481,7 @@ int run_gqa(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &v
     cp.min_tiles = p.min_tiles;
     cp.q_len = 1;
     cp.window = 0;
+    cp.start_align = 0;
     cp.unit_split = 0;
     const int rows = p.g < C::HEADS ? p.g : C::HEADS;
     return launch_combine(D, cp, p.B * units_per_seq, rows, stream,
@@ -485,10 +490,10 @@ int run_gqa(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &v
 
 // The tcgen05 kernel (gqa_tc_decode.cuh): tokens on the MMA rows, up to 64 query heads
 // per unit, NR head columns processed.
-template <int NR, bool KV8>
-int run_gqa_tc(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &vmap,
+template <int NR, bool KV8, bool RS = false>
+int run_gqa_tc(const typename GqaParamsOf<RS>::type &base, const CUtensorMap &kmap, const CUtensorMap &vmap,
                const CUtensorMap &qmap, DeviceState *dev, int units_per_seq, cudaStream_t stream) {
-    GqaParams p = base;
+    typename GqaParamsOf<RS>::type p = base;
     p.unit_split = 1;   // equal units are cut into parts of one unit each (schedule.cuh)
     const int smem = gqatc::smem_bytes(p.B);
     if (smem > dev->max_smem_optin) {
@@ -520,7 +525,8 @@ int run_gqa_tc(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap
     p.ws_o = reinterpret_cast<float *>(static_cast<char *>(ws) + meta_bytes + lse_bytes);
 
     // several new tokens or a window: the instantiation with the visibility mask
-    auto kern = (p.q_len > 1 || p.window > 0) ? gqa_tc_decode_kernel<NR, KV8, true> : gqa_tc_decode_kernel<NR, KV8, false>;
+    auto kern = (p.q_len > 1 || p.window > 0) ? gqa_tc_decode_kernel<NR, KV8, true, RS>
+                                              : gqa_tc_decode_kernel<NR, KV8, false, RS>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), dev, smem);
     if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(gqa tc)");
     kern<<<p.workers, gqatc::Cfg<NR, KV8>::NTHREADS, smem, stream>>>(p, kmap, vmap, qmap);
@@ -547,10 +553,12 @@ int run_gqa_tc(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap
     cp.min_tiles = p.min_tiles;
     cp.q_len = p.q_len;
     cp.window = p.window;
+    cp.start_align = 0;
+    if constexpr (RS) cp.start_align = p.start_align;
     cp.unit_split = p.unit_split;
     const int rows = p.g * p.q_len < gqatc::HB ? p.g * p.q_len : gqatc::HB;
     return launch_combine(gqatc::D, cp, p.B * units_per_seq, rows, stream,
-                          combine_warps((p.T_max + gqatc::TILE - 1) / gqatc::TILE, max_tiles, p.workers));
+                          combine_warps((p.T_max + gqatc::TILE - 1) / gqatc::TILE, max_tiles, p.workers), RS);
 }
 
 // Which GQA kernel runs: the tcgen05 kernel for head_dim 128 once a group has a few
@@ -575,6 +583,7 @@ struct GqaCache {
     bool e4m3 = false;            // E4M3 codes (value = code * scale) instead of bf16
     float k_scale = 1.f, v_scale = 1.f;
     bool one_page = false;        // every sequence's rows lie in its first page
+    const float *k_rows = nullptr, *v_rows = nullptr;   // a scale per cached row (E4M3; out is then bf16)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -725,7 +734,7 @@ int gqa_decode_impl(const uint16_t *q, const GqaCache &cache, const int32_t *seq
         if (st != KVATTN_OK) return st;
     } else if (tc) {
         // q [B, q_len, n_q, d]: box of the group's g heads at all q_len positions
-        st = make_map_4d(&qmap, q, head_dim, n_q_heads, q_len, batch, 64, g, q_len, CU_TENSOR_MAP_SWIZZLE_128B);
+        st = make_map_4d(&qmap, q, head_dim, n_q_heads, q_len, batch, 64, g, q_len, 1, CU_TENSOR_MAP_SWIZZLE_128B);
         if (st != KVATTN_OK) return st;
     }
 
@@ -750,6 +759,18 @@ int gqa_decode_impl(const uint16_t *q, const GqaCache &cache, const int32_t *seq
     p.v_scale = cache.v_scale;
     const int U = n_kv_heads * n_hb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tc && cache.k_rows) {
+        GqaRowScaleParams rp = {};
+        static_cast<GqaParams &>(rp) = p;
+        rp.k_rows = cache.k_rows;
+        rp.v_rows = cache.v_rows;
+        rp.pages = (int)cache.pages;
+        rp.start_align = cache.block_table && !cache.one_page ? gqatc::TILE : 0;
+        if (gl > 32) return run_gqa_tc<64, true, true>(rp, kmap, vmap, qmap, dev, U, s);
+        if (gl > 16) return run_gqa_tc<32, true, true>(rp, kmap, vmap, qmap, dev, U, s);
+        if (gl > 8) return run_gqa_tc<16, true, true>(rp, kmap, vmap, qmap, dev, U, s);
+        return run_gqa_tc<8, true, true>(rp, kmap, vmap, qmap, dev, U, s);
+    }
     if (tc && cache.e4m3) {
         if (gl > 32) return run_gqa_tc<64, true>(p, kmap, vmap, qmap, dev, U, s);
         if (gl > 16) return run_gqa_tc<32, true>(p, kmap, vmap, qmap, dev, U, s);
@@ -1509,3 +1530,5 @@ extern "C" int kvattn_gqa_decode_noalloc(const uint16_t *q, const uint16_t *k_ca
     return gqa_decode_impl(q, cache, seq_lens, batch, n_q_heads, n_kv_heads, head_dim, scale, out, lse, stream,
                            1, 0, true);
 }
+
+#include "serving_api.cuh"
