@@ -636,60 +636,65 @@ def kvattn_gqa_decode_multi(q, k_cache, v_cache, seq_lens, scale, window=0, out=
     return out, lse
 
 
-class _On:
-    """Runs a call on its stream and on its tensors' device: what it allocates belongs to that
-    stream.  The stream is the given one, else the device's current one."""
+# ---- the serving operators (a decode step calls them with a dozen tensors each, and the
+# smallest of their kernels take a few microseconds: the checks below are written to cost
+# little when they pass; what fails goes to the explaining ones above)
 
-    def __init__(self, device, stream):
+
+def _raw_stream(index):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(t, stream):
+    """None when a call on t can be made as things stand: t is on the current device and no
+    stream is given.  Otherwise the contexts under which it can: what the call allocates then
+    belongs to that stream."""
+    import torch
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)       # (makes the stream's device current too)
+
+
+def _at(t, name, dtype, shape, index):
+    """Address of a dense tensor of this type and shape on device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _codes_at(t, name, shape, index):
+    """Address of E4M3 codes (float8_e4m3fn or uint8)."""
+    if t.shape == shape and t.element_size() == 1 and t.get_device() == index and t.is_contiguous():
         import torch
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self._device = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-        self._stream = torch.cuda.stream(stream) if stream is not None else None
-        self._handle_of = torch.cuda.current_stream
-
-    def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
-        return ctypes.c_void_p(self._handle_of().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+        if t.dtype in (torch.float8_e4m3fn, torch.uint8):
+            return t.data_ptr()
+    _check_e4m3(t, name, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _check_on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _check_rows(t, name, shape):
-    """bf16 [N, heads, d], each token's heads dense, tokens any stride apart; returns the stride."""
+def _rows_at(t, name, dtype, shape, index):
+    """(address, stride) of bf16 [n, heads, d], each token's heads dense, tokens any stride apart."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     n, h, d = shape
     s = t.stride()
     if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
         raise ValueError(f"{name}'s heads must be dense within a token")
-    return s[0] if n > 1 else h * d
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return t.data_ptr(), s[0] if n > 1 else h * d
 
 
 def kvattn_rope_append_rowscale(q, k_new, v_new, positions, slots, k_pages, v_pages, k_scales, v_scales,
@@ -701,36 +706,36 @@ def kvattn_rope_append_rowscale(q, k_new, v_new, positions, slots, k_pages, v_pa
     [P, n_kv, page_size] fp32.  rope_base 0: no rotation (positions may be None).  q is rotated
     in place unless q_out is given; returns the rotated queries (None without q)."""
     import torch
+    cm = _elsewhere(k_new, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_rope_append_rowscale(q, k_new, v_new, positions, slots, k_pages, v_pages, k_scales, v_scales,
+                                               rope_base, interleaved, q_out)
+    bf16, f32 = torch.bfloat16, torch.float32
+    ix = k_new.get_device()
     N, n_kv, d = k_new.shape
-    P, S = k_pages.shape[0], k_pages.shape[2]
-    dev = k_new.device
-    ks = _check_rows(k_new, "k_new", (N, n_kv, d))
-    vs = _check_rows(v_new, "v_new", (N, n_kv, d))
-    n_q, qs, os_ = 0, 0, 0
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-    else:
+    P, _, S, _ = k_pages.shape
+    kv, pages, rows = (N, n_kv, d), (P, n_kv, S, d), (P, n_kv, S)
+    kn, ks = _rows_at(k_new, "k_new", bf16, kv, ix)
+    vn, vs = _rows_at(v_new, "v_new", bf16, kv, ix)
+    n_q = qa = qs = qo = qos = 0
+    if q is not None:
         n_q = q.shape[1]
-        q_out = q if q_out is None else q_out
-        qs = _check_rows(q, "q", (N, n_q, d))
-        os_ = _check_rows(q_out, "q_out", (N, n_q, d))
-    if positions is not None:
-        _check(positions, "positions", torch.int32, (N,))
-    _check(slots, "slots", torch.int64, (N,))
-    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
-    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
-    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
-    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
-    _check_on(dev, q=q, q_out=q_out, v_new=v_new, positions=positions, slots=slots, k_pages=k_pages, v_pages=v_pages,
-              k_scales=k_scales, v_scales=v_scales)
+        qa, qs = qo, qos = _rows_at(q, "q", bf16, (N, n_q, d), ix)
+        if q_out is None:
+            q_out = q
+        elif q_out is not q:
+            qo, qos = _rows_at(q_out, "q_out", bf16, (N, n_q, d), ix)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pos = None if positions is None else _at(positions, "positions", torch.int32, (N,), ix)
+    args = (qa or None, kn, vn, pos, _at(slots, "slots", torch.int64, (N,), ix), qo or None,
+            _codes_at(k_pages, "k_pages", pages, ix), _codes_at(v_pages, "v_pages", pages, ix),
+            _at(k_scales, "k_scales", f32, rows, ix), _at(v_scales, "v_scales", f32, rows, ix), N, n_q, n_kv, d, qs, qos,
+            ks, vs, P, S, rope_base, 1 if interleaved else 0, _raw_stream(ix))
     if N == 0:
         return q_out
-    with _On(dev, stream) as st:
-        rc = lib().kvattn_rope_append_rowscale(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), _ptr(positions),
-                                               slots.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
-                                               k_scales.data_ptr(), v_scales.data_ptr(), N, n_q, n_kv, d, qs, os_, ks,
-                                               vs, P, S, float(rope_base), int(bool(interleaved)), st)
+    rc = lib().kvattn_rope_append_rowscale(*args)
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_rope_append_rowscale")
     return q_out
@@ -741,47 +746,52 @@ def kvattn_gather_rowscale(k_pages, v_pages, k_scales, v_scales, slots, k_out=No
     kvattn_gather_rowscale): slots [N] int64.  Returns (k, v) [n_kv, N, d] bf16; k_out / v_out
     may be given, also as parts k_prefix[:, a:a + N] of longer buffers."""
     import torch
-    P, n_kv, S, d = k_pages.shape
+    cm = _elsewhere(k_pages, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_gather_rowscale(k_pages, v_pages, k_scales, v_scales, slots, k_out, v_out)
+    f32 = torch.float32
+    ix = k_pages.get_device()
+    pages = k_pages.shape
+    P, n_kv, S, d = pages
     N = slots.shape[0]
-    dev = k_pages.device
-    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
-    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
-    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
-    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
-    _check(slots, "slots", torch.int64, (N,))
-    with _On(dev, stream) as st:
-        if k_out is None:
-            k_out = torch.empty((n_kv, N, d), dtype=torch.bfloat16, device=dev)
-        if v_out is None:
-            v_out = torch.empty((n_kv, N, d), dtype=torch.bfloat16, device=dev)
-        kh = _check_rows(k_out, "k_out", (n_kv, N, d))
-        vh = _check_rows(v_out, "v_out", (n_kv, N, d))
-        _check_on(dev, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, slots=slots, k_out=k_out, v_out=v_out)
-        if N == 0:
-            return k_out, v_out
-        rc = lib().kvattn_gather_rowscale(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-                                          v_scales.data_ptr(), slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), N,
-                                          n_kv, d, kh, vh, P, S, st)
+    out, rows = (n_kv, N, d), (P, n_kv, S)
+    if k_out is None:
+        k_out = torch.empty(out, dtype=torch.bfloat16, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty(out, dtype=torch.bfloat16, device=k_pages.device)
+    ko, kh = _rows_at(k_out, "k_out", torch.bfloat16, out, ix)
+    vo, vh = _rows_at(v_out, "v_out", torch.bfloat16, out, ix)
+    args = (_codes_at(k_pages, "k_pages", pages, ix), _codes_at(v_pages, "v_pages", pages, ix),
+            _at(k_scales, "k_scales", f32, rows, ix), _at(v_scales, "v_scales", f32, rows, ix),
+            _at(slots, "slots", torch.int64, (N,), ix), ko, vo, N, n_kv, d, kh, vh, P, S, _raw_stream(ix))
+    if N == 0:
+        return k_out, v_out
+    rc = lib().kvattn_gather_rowscale(*args)
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gather_rowscale")
     return k_out, v_out
 
 
-def _outputs(q, out, lse):
-    """bf16 out like q and fp32 lse without its last axis, allocated where not given."""
-    import torch
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    _check(out, "out", torch.bfloat16, q.shape)
-    _check(lse, "lse", torch.float32, q.shape[:-1])
-    return out, lse
-
-
 def _q_shape(q):
     """(B, L, n_q, d) of q [B, n_q, d] or [B, L, n_q, d]."""
-    return (q.shape[0], 1, q.shape[1], q.shape[2]) if q.dim() == 3 else tuple(q.shape)
+    s = q.shape
+    if len(s) == 4:
+        return s
+    B, n_q, d = s
+    return B, 1, n_q, d
+
+
+def _outputs(q, out, lse, index):
+    """(out, lse, address, address): bf16 like q and fp32 without its last axis, allocated
+    where not given."""
+    import torch
+    s = q.shape
+    if out is None:
+        out = torch.empty(s, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(s[:-1], dtype=torch.float32, device=q.device)
+    return out, lse, _at(out, "out", torch.bfloat16, s, index), _at(lse, "lse", torch.float32, s[:-1], index)
 
 
 def kvattn_gqa_decode_rowscale(q, k_pages, v_pages, k_scales, v_scales, seq_lens, scale, block_table=None, window=0,
@@ -792,25 +802,26 @@ def kvattn_gqa_decode_rowscale(q, k_pages, v_pages, k_scales, v_scales, seq_lens
     [B, max_pages] int32, or without it [B, n_kv, T, 128] and [B, n_kv, T].  Returns (out bf16
     like q, lse fp32)."""
     import torch
+    cm = _elsewhere(q, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_gqa_decode_rowscale(q, k_pages, v_pages, k_scales, v_scales, seq_lens, scale, block_table,
+                                              window, out, lse)
+    f32, i32 = torch.float32, torch.int32
+    ix = q.get_device()
     B, L, n_q, d = _q_shape(q)
     P, n_kv, S, _ = k_pages.shape
-    M = block_table.shape[1] if block_table is not None else 1
-    dev = q.device
-    _check(q, "q", torch.bfloat16)
-    _check_e4m3(k_pages, "k_pages", (P, n_kv, S, d))
-    _check_e4m3(v_pages, "v_pages", (P, n_kv, S, d))
-    _check(k_scales, "k_scales", torch.float32, (P, n_kv, S))
-    _check(v_scales, "v_scales", torch.float32, (P, n_kv, S))
-    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    pages, rows = (P, n_kv, S, d), (P, n_kv, S)
+    table, M = None, 1
     if block_table is not None:
-        _check(block_table, "block_table", torch.int32, (B, M))
-    with _On(dev, stream) as st:
-        out, lse = _outputs(q, out, lse)
-        _check_on(dev, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, seq_lens=seq_lens,
-                  block_table=block_table, out=out, lse=lse)
-        rc = lib().kvattn_gqa_decode_rowscale(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-                                              v_scales.data_ptr(), _ptr(block_table), seq_lens.data_ptr(), P, S, M, B, L,
-                                              n_q, n_kv, d, float(scale), int(window), out.data_ptr(), lse.data_ptr(), st)
+        M = block_table.shape[1]
+        table = _at(block_table, "block_table", i32, (B, M), ix)
+    out, lse, oa, la = _outputs(q, out, lse, ix)
+    rc = lib().kvattn_gqa_decode_rowscale(
+        _at(q, "q", torch.bfloat16, q.shape, ix), _codes_at(k_pages, "k_pages", pages, ix),
+        _codes_at(v_pages, "v_pages", pages, ix), _at(k_scales, "k_scales", f32, rows, ix),
+        _at(v_scales, "v_scales", f32, rows, ix), table, _at(seq_lens, "seq_lens", i32, (B,), ix), P, S, M, B, L, n_q, n_kv,
+        d, scale, window, oa, la, _raw_stream(ix))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gqa_decode_rowscale")
     return out, lse
@@ -823,19 +834,19 @@ def kvattn_gqa_decode_prefix_workspace(max_prefix_len, max_seq_len, batch, q_len
                                                   head_dim, ctypes.byref(n))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gqa_decode_prefix_workspace")
-    return int(n.value)
+    return n.value
 
 
-def _workspace(workspace, need, dev):
+def _workspace(workspace, q, index, *sizes):
     """The caller's workspace, or one of torch's allocator for this call alone (stream-ordered;
-    inside a graph capture it belongs to the graph)."""
+    inside a graph capture it belongs to the graph): the tensor and its bytes."""
     import torch
     if workspace is None:
-        return torch.empty((need,), dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", torch.uint8)
-    if workspace.dim() != 1 or workspace.numel() < need:
-        raise ValueError(f"workspace must be a vector of at least {need} bytes")
-    return workspace
+        workspace = torch.empty((kvattn_gqa_decode_prefix_workspace(*sizes),), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or workspace.dim() != 1 or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense uint8 vector on cuda:{index}")
+    return workspace, workspace.shape[0]
 
 
 def kvattn_gqa_decode_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, scale, out=None, lse=None,
@@ -843,28 +854,27 @@ def kvattn_gqa_decode_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache
     """Decode for a batch that shares a prefix (include/kvattn.h, kvattn_gqa_decode_prefix): q
     [B, n_q, d] or [B, L, n_q, d] bf16, k_prefix / v_prefix [n_kv, P, d] bf16 with prefix_len [1]
     int32, k_cache / v_cache [B, n_kv, T, d] bf16 with seq_lens [B] int32.  Returns (out bf16 like
-    q, lse fp32).  workspace: uint8, kvattn_gqa_decode_prefix_workspace bytes."""
+    q, lse fp32).  workspace: uint8, kvattn_gqa_decode_prefix_workspace bytes (KvattnError if it
+    is too small)."""
     import torch
+    cm = _elsewhere(q, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_gqa_decode_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, scale, out, lse,
+                                            workspace)
+    bf16, i32 = torch.bfloat16, torch.int32
+    ix = q.get_device()
     B, L, n_q, d = _q_shape(q)
     n_kv, P, _ = k_prefix.shape
     T = k_cache.shape[2]
-    dev = q.device
-    _check(q, "q", torch.bfloat16)
-    _check(k_prefix, "k_prefix", torch.bfloat16, (n_kv, P, d))
-    _check(v_prefix, "v_prefix", torch.bfloat16, (n_kv, P, d))
-    _check(prefix_len, "prefix_len", torch.int32, (1,))
-    _check(k_cache, "k_cache", torch.bfloat16, (B, n_kv, T, d))
-    _check(v_cache, "v_cache", torch.bfloat16, (B, n_kv, T, d))
-    _check(seq_lens, "seq_lens", torch.int32, (B,))
-    with _On(dev, stream) as st:
-        out, lse = _outputs(q, out, lse)
-        ws = _workspace(workspace, kvattn_gqa_decode_prefix_workspace(P, T, B, L, n_q, n_kv, d), dev)
-        _check_on(dev, k_prefix=k_prefix, v_prefix=v_prefix, prefix_len=prefix_len, k_cache=k_cache, v_cache=v_cache,
-                  seq_lens=seq_lens, out=out, lse=lse, workspace=ws)
-        rc = lib().kvattn_gqa_decode_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), prefix_len.data_ptr(),
-                                            P, k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(), T, B, L, n_q,
-                                            n_kv, d, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                            ws.numel(), st)
+    prefix, own = (n_kv, P, d), (B, n_kv, T, d)
+    args = (_at(q, "q", bf16, q.shape, ix), _at(k_prefix, "k_prefix", bf16, prefix, ix),
+            _at(v_prefix, "v_prefix", bf16, prefix, ix), _at(prefix_len, "prefix_len", i32, (1,), ix), P,
+            _at(k_cache, "k_cache", bf16, own, ix), _at(v_cache, "v_cache", bf16, own, ix),
+            _at(seq_lens, "seq_lens", i32, (B,), ix), T, B, L, n_q, n_kv, d, scale)
+    out, lse, oa, la = _outputs(q, out, lse, ix)
+    ws, size = _workspace(workspace, q, ix, P, T, B, L, n_q, n_kv, d)
+    rc = lib().kvattn_gqa_decode_prefix(*args, oa, la, ws.data_ptr(), size, _raw_stream(ix))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gqa_decode_prefix")
     return out, lse
@@ -876,46 +886,41 @@ def kvattn_gqa_decode_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len
     kvattn_gqa_decode_prefix_paged): k_pages / v_pages [num_pages, n_kv, page_size, d] bf16,
     prefix_table [max_prefix_pages] and block_table [B, max_pages] int32."""
     import torch
+    cm = _elsewhere(q, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_gqa_decode_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens,
+                                                  scale, out, lse, workspace)
+    bf16, i32 = torch.bfloat16, torch.int32
+    ix = q.get_device()
     B, L, n_q, d = _q_shape(q)
     N, n_kv, S, _ = k_pages.shape
     PM, M = prefix_table.shape[0], block_table.shape[1]
-    dev = q.device
-    _check(q, "q", torch.bfloat16)
-    _check(k_pages, "k_pages", torch.bfloat16, (N, n_kv, S, d))
-    _check(v_pages, "v_pages", torch.bfloat16, (N, n_kv, S, d))
-    _check(prefix_table, "prefix_table", torch.int32, (PM,))
-    _check(prefix_len, "prefix_len", torch.int32, (1,))
-    _check(block_table, "block_table", torch.int32, (B, M))
-    _check(seq_lens, "seq_lens", torch.int32, (B,))
-    with _On(dev, stream) as st:
-        out, lse = _outputs(q, out, lse)
-        ws = _workspace(workspace, kvattn_gqa_decode_prefix_workspace(PM * S, M * S, B, L, n_q, n_kv, d), dev)
-        _check_on(dev, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table, prefix_len=prefix_len,
-                  block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=ws)
-        rc = lib().kvattn_gqa_decode_prefix_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                                  prefix_table.data_ptr(), prefix_len.data_ptr(), PM,
-                                                  block_table.data_ptr(), seq_lens.data_ptr(), N, S, M, B, L, n_q, n_kv,
-                                                  d, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                                  ws.numel(), st)
+    pages = (N, n_kv, S, d)
+    args = (_at(q, "q", bf16, q.shape, ix), _at(k_pages, "k_pages", bf16, pages, ix),
+            _at(v_pages, "v_pages", bf16, pages, ix), _at(prefix_table, "prefix_table", i32, (PM,), ix),
+            _at(prefix_len, "prefix_len", i32, (1,), ix), PM, _at(block_table, "block_table", i32, (B, M), ix),
+            _at(seq_lens, "seq_lens", i32, (B,), ix), N, S, M, B, L, n_q, n_kv, d, scale)
+    out, lse, oa, la = _outputs(q, out, lse, ix)
+    ws, size = _workspace(workspace, q, ix, PM * S, M * S, B, L, n_q, n_kv, d)
+    rc = lib().kvattn_gqa_decode_prefix_paged(*args, oa, la, ws.data_ptr(), size, _raw_stream(ix))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gqa_decode_prefix_paged")
     return out, lse
 
 
-def _check_probs(t, name, dtype, shape):
-    """Probabilities [B, L, V], the vocabulary contiguous; returns the other axes' strides."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != dtype:
+def _probs_at(t, name, dtype, shape, index):
+    """(address, stride, stride) of probabilities [B, L, V], the vocabulary contiguous."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if shape[2] > 1 and t.stride(2) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    b, l, v = t.stride()
+    if v != 1 and shape[2] > 1:
         raise ValueError(f"{name}'s vocabulary axis must be contiguous")
-    return t.stride(0), t.stride(1)
+    return t.data_ptr(), b, l
 
 
 def kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, draft_lens=None, accepted=None,
@@ -926,30 +931,29 @@ def kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sa
     None.  Rows may be strided (a padded vocabulary).  Returns (accepted [B], tokens [B, L + 1])
     int32."""
     import torch
+    dtype = target_probs.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise ValueError(f"target_probs must be float32 or bfloat16, got {dtype}")
+    cm = _elsewhere(target_probs, stream)
+    if cm is not None:
+        with cm:
+            return kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, draft_lens, accepted,
+                                        tokens)
+    f32, i32 = torch.float32, torch.int32
+    ix = target_probs.get_device()
     B, L1, V = target_probs.shape
     L = L1 - 1
-    dtype, dev = target_probs.dtype, target_probs.device
-    if dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"target_probs must be float32 or bfloat16, got {dtype}")
-    tb, tl = _check_probs(target_probs, "target_probs", dtype, (B, L1, V))
-    db, dl = _check_probs(draft_probs, "draft_probs", dtype, (B, L, V)) if draft_probs is not None else (0, 0)
-    _check(draft_tokens, "draft_tokens", torch.int32, (B, L))
-    _check(u_accept, "u_accept", torch.float32, (B, L))
-    _check(u_sample, "u_sample", torch.float32, (B,))
-    if draft_lens is not None:
-        _check(draft_lens, "draft_lens", torch.int32, (B,))
-    with _On(dev, stream) as st:
-        if accepted is None:
-            accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-        if tokens is None:
-            tokens = torch.empty((B, L1), dtype=torch.int32, device=dev)
-        _check(accepted, "accepted", torch.int32, (B,))
-        _check(tokens, "tokens", torch.int32, (B, L1))
-        _check_on(dev, draft_probs=draft_probs, draft_tokens=draft_tokens, u_accept=u_accept, u_sample=u_sample,
-                  draft_lens=draft_lens, accepted=accepted, tokens=tokens)
-        rc = lib().kvattn_verify_drafts(target_probs.data_ptr(), _ptr(draft_probs), draft_tokens.data_ptr(),
-                                        _ptr(draft_lens), u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(),
-                                        tokens.data_ptr(), B, L, V, int(dtype == torch.bfloat16), tb, tl, db, dl, st)
+    pa, pb, pl = _probs_at(target_probs, "target_probs", dtype, (B, L1, V), ix)
+    qa, qb, ql = (None, 0, 0) if draft_probs is None else _probs_at(draft_probs, "draft_probs", dtype, (B, L, V), ix)
+    lens = None if draft_lens is None else _at(draft_lens, "draft_lens", i32, (B,), ix)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=i32, device=target_probs.device)
+    if tokens is None:
+        tokens = torch.empty((B, L1), dtype=i32, device=target_probs.device)
+    rc = lib().kvattn_verify_drafts(pa, qa, _at(draft_tokens, "draft_tokens", i32, (B, L), ix), lens,
+                                    _at(u_accept, "u_accept", f32, (B, L), ix), _at(u_sample, "u_sample", f32, (B,), ix),
+                                    _at(accepted, "accepted", i32, (B,), ix), _at(tokens, "tokens", i32, (B, L1), ix), B, L,
+                                    V, 1 if dtype is torch.bfloat16 else 0, pb, pl, qb, ql, _raw_stream(ix))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_verify_drafts")
     return accepted, tokens

@@ -138,7 +138,7 @@ def test_three_dim_query_and_own_workspace():
                                            lens, 0.1, workspace=ws)
     torch.cuda.synchronize()
     check(x, out[:, None], lse[:, None], 0.1)
-    with pytest.raises(ValueError):
+    with pytest.raises(kb.KvattnError):
         kb.kvattn_gqa_decode_prefix(dev["q"], dev["kp"], dev["vp"], plen, dev["ks"], dev["vs"], lens, 0.1, workspace=ws[:-1])
 
 
