@@ -14,28 +14,46 @@
 // one sequence's L * g rows in the tile.
 //
 // Work.  A unit is (KV head, pair of 128-row tiles) over the prefix, or (sequence, KV head)
-// over a suffix; each unit is a run of 128-token K/V tiles.  All units are laid end to end --
-// a prefix tile that serves two row tiles counts twice -- and worker w (one CTA per SM) takes
-// an equal contiguous range of that line, computed on the device from prefix_len and seq_lens
-// (so a captured call may be replayed with other lengths).  Prefix and suffix work thus run side by
-// side: some SMs keep the tensor cores busy while others stream suffixes from memory.  Every
-// piece (a worker's part of a unit) leaves a normalised partial and its log-sum-exp in the
-// caller's workspace; prefix_merge_kernel joins a row's partials.
+// over a suffix; each unit is a run of 128-token K/V tiles.  All units are laid end to end on a
+// line whose positions stand for time -- WP2 a prefix tile that serves two row tiles, WP1 one that
+// serves one, WS a suffix tile, and one tile more for each unit, whose start and end cost about
+// that -- and worker w (one CTA per SM) takes an equal contiguous range of it, computed on
+// the device from prefix_len and seq_lens (so a captured call may be replayed with other
+// lengths).  Prefix and suffix work thus run side by side: some SMs keep the tensor cores busy
+// while others stream suffixes from memory.  Every piece (a worker's part of a unit) leaves a
+// normalised partial and its log-sum-exp in the caller's workspace; prefix_merge_kernel joins a
+// row's partials.
 //
 // Pipeline of a CTA (384 threads):
 //   warp 0       producer: TMA loads (128-byte swizzle, no multicast) of Q tiles and of K and
 //                V tiles into a ring.
-//   warp 1       one thread issues every tcgen05.mma: S_x = Q K^T (A, B from shared memory) and
-//                O_x += P_x V (P_x read from tensor memory, V tile MN-major).
+//   warps 1, 2   one thread each issues the tcgen05.mma of group x = 0, 1: S_x = Q K^T (A, B from
+//                shared memory) and O_x += P_x V (P_x read from tensor memory, V tile MN-major).
 //   warps 4..11  two softmax groups x = 0, 1 of 128 threads, one thread per row: a row's 128
-//                scores are one TMEM lane, so its maximum and sum need no exchange.  P_x
-//                (bf16) overwrites the first half of S_x.
+//                scores are one TMEM lane, so its maximum and sum need no exchange.  P_x (bf16)
+//                overwrites S_x.  They also release the K, V and Q tiles, since the commit that
+//                announces scores tells them that the products before are done.
 // Steps alternate between the groups, so that one group's exponentials run while the tensor
 // cores work for the other: in a two-row-tile unit the groups hold the two row tiles and
 // each K/V tile makes two steps; in a one-row-tile unit both groups hold the same rows and take
 // alternate K/V tiles, each with its own (max, sum, O), which the merge joins.
-// The running maximum moves lazily: only when a row's tile maximum exceeds it by 2^8 are that
-// row's O and sum rescaled.
+//
+// A group's step is a chain: scores, exponentials, weights times V, next scores (tensor memory
+// has no room for a second score buffer), so its length bounds the kernel.  Two things shorten it.
+// The weights are taken against the running maximum of the steps before, so no exponential waits
+// for this step's; the maximum moves afterwards, when a row's scores have exceeded it by more
+// than 2^8 (its O and sum are then rescaled before the next step's product), and at once only on
+// a piece's first step and where they exceed it by 2^LIMIT.  And the weights are handed over in two
+// halves of 64 tokens, the first half's product running under the second half's exponentials.
+// Measured on 64 sequences of 64 heads behind 32768 tokens, cycles a pair of steps (the products
+// alone: 2048):
+//   one issuer for both groups                6200  eight MMAs take ~600 to issue, a commit ~180
+//   an issuer a group, issuing freely         5500  the groups' products interleave, both end late,
+//                                                   and the groups fall into step
+//   ... in turns                              4250
+//   steps in halves, a score buffer each      3900  the score products of N = 64 are bound by shared
+//                                                   memory, which also takes the TMA writes
+//   two threads a row                         4400  a swap of maxima, and registers that do not reach
 // Weights enter the value product rounded to bf16 (half a step, 2^-9 relative, each independent
 // of the others; the output is rounded to bf16 itself); sums, maxima and O are fp32.
 #pragma once
@@ -52,9 +70,9 @@ struct PrefixParams {
     const int32_t *block_table;    // [B, max_pages] or null: one page a sequence
     __nv_bfloat16 *out;            // [B, L, n_q, D]
     float *lse;                    // [B, L, n_q]
-    long long *meta;               // [0] tiles of the prefix, [1] W; then int suffix tile prefix [B + 1]
-    float *lse_p, *o_p;            // prefix partials [units_p + workers][2][128] (x D)
-    float *lse_s, *o_s;            // suffix partials [B * n_kv + workers][2][L * g] (x D)
+    uint32_t *meta;                // [0] tiles of the prefix; from [2] on the suffix table [B + 1]
+    float *lse_p, *o_p;            // prefix partials [units_p + workers][2][128], [..][2][D][128]
+    float *lse_s, *o_s;            // suffix partials [B * n_kv + workers][2][L * g], [..][2][L * g][D]
     int B, L, n_q, n_kv, g;
     int P_max, T_max;              // capacities (lengths are clamped to them)
     int prefix_page, page_size;    // rows per page of the prefix's and the suffixes' cache
@@ -62,7 +80,7 @@ struct PrefixParams {
     int tok_tile;                  // new tokens in a row tile: floor(128 / g)
     int row_tiles, pairs;          // ceil(B L / tok_tile), ceil(row_tiles / 2)
     int workers;
-    int prefix_in_ws;              // the suffix tile prefix was written to the workspace before
+    int table_in_ws;               // the suffix table was written to the workspace before
     float scale_log2;              // scale * log2(e)
 };
 
@@ -71,30 +89,111 @@ namespace pfx {
 constexpr int TILE = 128;
 constexpr int ROWS = 128;
 constexpr int NTHREADS = 384;
-// registers of a thread after the split between the first warpgroup (producer, issuer) and the
+// registers of a thread after the split between the first warpgroup (producer, issuers) and the
 // softmax warpgroups: a row's 128 scores and its packed weights stay in registers
-constexpr int REGS_CTRL = 80, REGS_SOFT = 208;
-static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= NTHREADS * 168, "registers of the launch");
+constexpr int REGS_LAUNCH = 168, REGS_CTRL = 80, REGS_SOFT = 208;
+static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= NTHREADS * REGS_LAUNCH, "registers of the launch");
 constexpr int CHUNK = 128 * 128;          // [128 rows x 128 bytes]
 constexpr int NS_MAX = 10;
-constexpr int MIN_TILES = 2;              // a worker takes at least two tiles
-constexpr float RESCALE = 8.f;
+constexpr float RESCALE = 8.f, LIMIT = 64.f;
+// Line positions (see above), and the least a worker takes.
+constexpr uint32_t WP2 = 4, WP1 = 2, WS = 4, W_MIN = 4;
+constexpr long long LINE_LIMIT = 1ll << 30;
+// Of every eight pairs of exponentials, this many are taken on the FMA pipe.
+constexpr int POLY = 0;
+
+// Two fp32 values in one 64-bit register pair: one instruction works on both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x of a pair on the FMA pipe (x <= 100; below -126 it is 2^-126, nothing next to a sum of weights):
+// x = n + r with n the nearest integer (adding 1.5 * 2^23 leaves n in the low mantissa bits),
+// 2^r for |r| <= 1/2 by a polynomial of degree 4 -- fitted to the least maximal relative error,
+// 2.6e-6, a hundredth of the weight's bf16 step -- and n added to its exponent field.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
+    float a, b;
+    unpack2(x2, a, b);
+    x2 = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+    const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
+    const uint64_t t = add2(x2, magic);
+    const uint64_t r = fma2(add2(t, unmagic), pack2(-1.f, -1.f), x2);
+    uint64_t y = pack2(0.00957010160f, 0.00957010160f);
+    y = fma2(y, r, pack2(0.0559178621f, 0.0559178621f));
+    y = fma2(y, r, pack2(0.240247448f, 0.240247448f));
+    y = fma2(y, r, pack2(0.693121815f, 0.693121815f));
+    y = fma2(y, r, pack2(0.999999261f, 0.999999261f));
+    float ta, tb, ya, yb;
+    unpack2(t, ta, tb);
+    unpack2(y, ya, yb);
+    return pack2(__uint_as_float(__float_as_uint(ya) + (__float_as_uint(ta) << 23)),
+                 __uint_as_float(__float_as_uint(yb) + (__float_as_uint(tb) << 23)));
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 
 template <int D>
 struct Cfg {
     static constexpr int NCH = D / 64;                  // 64-wide chunks of a row
     static constexpr int KV_BYTES = NCH * CHUNK;        // a K or V tile
     static constexpr int Q_BYTES = NCH * CHUNK;         // a Q tile
-    static constexpr int NS = (160 * 1024) / KV_BYTES;  // ring slots (K and V tiles alternate)
+    static constexpr uint32_t NS = (160 * 1024) / KV_BYTES;   // ring slots (K and V tiles alternate)
     static constexpr int OFF_Q = NS * KV_BYTES;
     static constexpr int OFF_BARS = OFF_Q + 2 * Q_BYTES;
-    static constexpr int OFF_PREFIX = OFF_BARS + 512;
-    // the suffix tile prefix lies in shared memory up to this batch, in the workspace beyond
-    static constexpr int B_SMEM = 320;
-    static constexpr int SMEM = 1024 + OFF_PREFIX + (B_SMEM + 1) * 4;
-    static_assert(SMEM <= 232448, "shared memory of an SM");
+    static constexpr int OFF_TABLE = OFF_BARS + 384;
+    // the suffix table lies in shared memory up to this batch, in the workspace beyond
+    static constexpr int B_SMEM = 640;
+    static constexpr int SMEM = OFF_TABLE + (B_SMEM + 1) * 4;
     static_assert(NS <= NS_MAX, "ring barriers");
+    static_assert(SMEM <= 232448, "shared memory of an SM");
 };
+
+// Operand descriptors (tc05.cuh, 128-byte swizzle, 8-row groups 1024 bytes apart) and MMAs from
+// their low words: an operand's steps differ there alone, by the step's offset in 16-byte units.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "n"(DESC_HI), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "n"(DESC_HI), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
 
 // tensor memory columns of group x: scores (and weights) at 128 x, output at 256 + 128 x
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_X = 128;
@@ -102,35 +201,90 @@ constexpr uint32_t TM_S = 0, TM_O = 256, TM_X = 128;
 struct Bars {
     uint64_t full[NS_MAX], empty[NS_MAX];
     uint64_t qfull[2], qempty[2];
-    uint64_t sready[2];      // scores of group x's next step are in TMEM (and its last value product is done)
-    uint64_t pready[2];      // group x has written its weights (and rescaled O_x)
+    uint64_t sready[2];      // group x's next scores are in TMEM (and its value product before is done)
+    uint64_t pready[2][2];   // [group][half] the weights are written (and O_x rescaled)
+    uint64_t turn[2];        // group x may issue its next products
     uint64_t odone[2];       // group x's last value product of a piece is done
     uint64_t ofree[2];       // group x has read O_x
     uint32_t tmem;
+    int prefix_len;
     int abort_flag;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block overflows its slot");
+static_assert(sizeof(Bars) <= 384, "barrier block overflows its slot");
 
-// The line of work, the same on every CTA and in the merge kernel.
+// ------------------------------------------------------------------ the line of work
+// The suffix table: word b holds, in its upper 25 bits, the sum over the sequences before b of
+// their line units c = tiles + 1 (0 without tokens), and in its lower 7 the last tile's tokens
+// less one: a sequence's tiles and length without another load.
+__device__ __forceinline__ uint32_t table_units(uint32_t w) { return w >> 7; }
+
+// Fills tab[0..B] by one warp.
+__device__ __forceinline__ void build_table(const int32_t *seq_lens, int B, int T_max, uint32_t *tab, int lane) {
+    uint32_t running = 0;
+    constexpr int U = 4;
+    for (int base = 0; base < B; base += 32 * U) {
+        int len[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + 32 * u + lane;
+            len[u] = i < B ? clamp_len(__ldg(seq_lens + i), T_max) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + 32 * u + lane;
+            const uint32_t nt = (uint32_t)tiles_of(len[u], TILE);
+            const uint32_t c = nt ? nt + 1 : 0;
+            uint32_t s = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, s, off);
+                if (lane >= off) s += y;
+            }
+            if (i < B) tab[i] = ((running + s - c) << 7) | (nt ? (uint32_t)(len[u] - 1) & 127u : 0u);
+            running += __shfl_sync(0xffffffffu, s, 31);
+        }
+    }
+    if (lane == 0) tab[B] = running << 7;
+}
+
+// The same on every CTA and in the merge kernel.
 struct Line {
-    int n_p;                 // prefix tiles
-    int wp;                  // line positions per prefix tile: 2 when row tiles pair up, else 1
-    long long units_p;
-    long long p_total;       // positions of the prefix units
-    long long total, W;
+    uint32_t n_p;            // prefix tiles
+    uint32_t wp;             // positions of a prefix tile
+    uint32_t unit_p;         // positions of a prefix unit
+    uint32_t p_total;        // of all of them
+    uint32_t total, W;
 };
-__device__ __forceinline__ Line make_line(const PrefixParams &p, int suffix_tiles) {
+__device__ __forceinline__ Line make_line(const PrefixParams &p, uint32_t n_p, uint32_t suffix_units) {
     Line l;
-    l.n_p = tiles_of(clamp_len(__ldg(p.prefix_len), p.P_max), TILE);
-    l.wp = p.row_tiles > 1 ? 2 : 1;
-    l.units_p = (long long)p.n_kv * p.pairs;
-    l.p_total = l.units_p * l.n_p * l.wp;
-    l.total = l.p_total + (long long)suffix_tiles * p.n_kv;
+    l.n_p = n_p;
+    l.wp = p.row_tiles > 1 ? WP2 : WP1;
+    l.unit_p = n_p ? (n_p + 1) * l.wp : 0;
+    l.p_total = (uint32_t)(p.n_kv * p.pairs) * l.unit_p;
+    l.total = l.p_total + suffix_units * (uint32_t)p.n_kv * WS;
     l.W = (l.total + p.workers - 1) / p.workers;
-    if (l.W < MIN_TILES) l.W = MIN_TILES;
-    l.W = (l.W + 1) & ~1ll;              // (no boundary inside a prefix tile)
+    if (l.W < W_MIN) l.W = W_MIN;
     return l;
 }
+// Tiles of a unit (nt tiles of WT positions from u0 on) that start in worker w's range.
+template <uint32_t WT>
+__device__ __forceinline__ void piece_tiles_of(const Line &l, uint32_t u0, uint32_t nt, uint32_t w, uint32_t &lt0, uint32_t &lt1) {
+    const uint32_t a = w * l.W, b = a + l.W;
+    lt0 = a <= u0 ? 0u : min(nt, (a - u0 + WT - 1) / WT);
+    lt1 = b <= u0 ? 0u : min(nt, (b - u0 + WT - 1) / WT);
+}
+__device__ __forceinline__ void prefix_piece(const Line &l, uint32_t u0, uint32_t w, uint32_t &lt0, uint32_t &lt1) {
+    if (l.wp == WP2) piece_tiles_of<WP2>(l, u0, l.n_p, w, lt0, lt1);
+    else piece_tiles_of<WP1>(l, u0, l.n_p, w, lt0, lt1);
+}
+__device__ __forceinline__ void suffix_piece(const Line &l, uint32_t u0, uint32_t nt, uint32_t w, uint32_t &lt0, uint32_t &lt1) {
+    piece_tiles_of<WS>(l, u0, nt, w, lt0, lt1);
+}
+
+// In a suffix the two groups hold the same few rows: group 1 holds them `shift` lanes further up,
+// so that the groups' warps that work lie on different schedulers.  Its Q operand starts that
+// many rows before the tile (in shared memory of the CTA; those lanes are not read).
+__device__ __forceinline__ int suffix_shift(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 0; }
 
 struct Piece {
     bool prefix;
@@ -141,56 +295,103 @@ struct Piece {
     int len;             // tokens of the unit
     int lt0, lt1;        // its tiles
     int steps;
-    long long slot;      // partial
+    uint32_t slot;       // partial
 };
 
-// The piece of worker w that starts at line position pos; pos moves to its end.
-__device__ __forceinline__ Piece next_piece(const PrefixParams &p, const Line &l, const int *s_prefix, long long &pos,
-                                            long long end, int w) {
-    Piece c;
-    if (pos < l.p_total) {
-        const long long ul = (long long)l.n_p * l.wp;
-        const long long u = pos / ul;
-        const long long u0 = u * ul;
-        const long long stop = end < u0 + ul ? end : u0 + ul;
-        c.prefix = true;
-        c.j = (int)(u / p.pairs);
-        c.pair = (int)(u % p.pairs);
-        c.two = 2 * c.pair + 1 < p.row_tiles;
-        c.b = 0;
-        c.len = clamp_len(__ldg(p.prefix_len), p.P_max);
-        c.lt0 = (int)((pos - u0) / l.wp);
-        c.lt1 = (int)((stop - u0) / l.wp);
-        c.slot = u + w;
-        pos = stop;
-    } else {
-        const long long sp = pos - l.p_total;
-        c.prefix = false;
-        c.two = false;
-        c.b = find_seq(s_prefix, p.B, p.n_kv, sp);
-        const int nt = s_prefix[c.b + 1] - s_prefix[c.b];
-        const long long base = (long long)s_prefix[c.b] * p.n_kv;
-        c.j = (int)((sp - base) / nt);
-        c.pair = 0;
-        const long long u0 = l.p_total + base + (long long)c.j * nt;
-        const long long stop = end < u0 + nt ? end : u0 + nt;
-        c.len = clamp_len(__ldg(p.seq_lens + c.b), p.T_max);
-        c.lt0 = (int)(pos - u0);
-        c.lt1 = (int)(stop - u0);
-        c.slot = (long long)c.b * p.n_kv + c.j + w;
-        pos = stop;
+// A walk over worker w's pieces, with what the roles keep of the pieces before.
+struct Walk {
+    Piece pc;
+    uint32_t pos, end;       // line positions still to take
+    uint32_t u0, u1;         // the present unit's
+    uint32_t steps, tiles;   // of the pieces before (the steps' parity is the group that takes the first)
+    int qs;                  // Q slot of the piece's first row tile
+    uint32_t quse0, quse1;   // uses of each Q slot, this piece's included
+};
+__device__ __forceinline__ Walk walk_start(const Line &l, int w) {
+    Walk k;
+    k.pos = (uint32_t)w * l.W;
+    k.end = k.pos + l.W < l.total ? k.pos + l.W : l.total;
+    k.u0 = k.u1 = 0;
+    k.steps = k.tiles = 0;
+    k.qs = 0;
+    k.quse0 = k.quse1 = 0;
+    k.pc.steps = 0;
+    k.pc.lt0 = k.pc.lt1 = 0;
+    k.pc.two = true;
+    k.pc.prefix = true;
+    k.pc.b = k.pc.j = k.pc.pair = 0;
+    return k;
+}
+// Moves to the next piece with tiles; false after the last.
+__device__ __forceinline__ bool walk_next(Walk &k, const PrefixParams &p, const Line &l, const uint32_t *tab,
+                                          int prefix_len, int w) {
+    Piece &c = k.pc;
+    k.steps += (uint32_t)c.steps;
+    k.tiles += (uint32_t)(c.lt1 - c.lt0);
+    if (!c.two) k.qs ^= 1;
+    c.two = true;            // (skipped pieces take no slot)
+    while (k.pos < k.end) {
+        uint32_t a, b;
+        if (k.pos < l.p_total) {
+            const uint32_t ul = l.unit_p, u = k.pos / ul;
+            c.prefix = true;
+            c.j = (int)(u / (uint32_t)p.pairs);
+            c.pair = (int)u - c.j * p.pairs;
+            c.len = prefix_len;
+            c.slot = u + (uint32_t)w;
+            k.u0 = u * ul;
+            k.u1 = k.u0 + ul;
+            prefix_piece(l, k.u0, (uint32_t)w, a, b);
+        } else {
+            if (!c.prefix && c.j + 1 < p.n_kv && k.pos == k.u1) {
+                // the same sequence's next head
+                ++c.j;
+                const uint32_t ul = k.u1 - k.u0;
+                k.u0 = k.u1;
+                k.u1 += ul;
+            } else {
+                // the sequence at this position (the last one whose first unit is not past it)
+                const uint32_t at = (k.pos - l.p_total) / ((uint32_t)p.n_kv * WS);
+                int lo = 0, hi = p.B - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (table_units(tab[mid]) <= at) lo = mid; else hi = mid - 1;
+                }
+                c.b = lo;
+                const uint32_t w0 = tab[lo];
+                const uint32_t cu = table_units(tab[lo + 1]) - table_units(w0);
+                c.len = (int)((cu - 2) * TILE + (w0 & 127u) + 1);
+                c.j = (int)((k.pos - l.p_total - table_units(w0) * (uint32_t)p.n_kv * WS) / (cu * WS));
+                c.prefix = false;
+                k.u0 = l.p_total + (table_units(w0) * (uint32_t)p.n_kv + (uint32_t)c.j * cu) * WS;
+                k.u1 = k.u0 + cu * WS;
+            }
+            c.slot = (uint32_t)(c.b * p.n_kv + c.j + w);
+            suffix_piece(l, k.u0, (uint32_t)tiles_of(c.len, TILE), (uint32_t)w, a, b);
+        }
+        k.pos = k.u1 < k.end ? k.u1 : k.end;
+        if (a < b) {
+            c.lt0 = (int)a;
+            c.lt1 = (int)b;
+            c.two = c.prefix && 2 * c.pair + 1 < p.row_tiles;
+            c.steps = (c.lt1 - c.lt0) * (c.two ? 2 : 1);
+            if (c.two || k.qs == 0) ++k.quse0;
+            if (c.two || k.qs == 1) ++k.quse1;
+            return true;
+        }
     }
-    c.steps = (c.lt1 - c.lt0) * (c.two ? 2 : 1);
-    return c;
+    c.steps = 0;
+    c.lt0 = c.lt1 = 0;
+    return false;
 }
 
 struct Ctx {
     uint8_t *smem;
     Bars *bars;
     volatile int *abort_flag;
-    const int *s_prefix;
+    const uint32_t *tab;
     Line line;
-    long long p0, p1;
+    int prefix_len;
     int w;
 };
 
@@ -202,16 +403,16 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
     using C = Cfg<D>;
     Bars *bars = c.bars;
     const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
-    uint32_t quse[2] = {0, 0};
-    int qs = 0;
     uint32_t n = 0;                 // tiles (K and V) issued
     bool ok = true;
-    for (long long pos = c.p0; pos < c.p1 && ok;) {
-        const Piece pc = next_piece(p, c.line, c.s_prefix, pos, c.p1, c.w);
+    Walk k = walk_start(c.line, c.w);
+    while (ok && walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
+        const Piece &pc = k.pc;
         const int nq = pc.two ? 2 : 1;
         for (int r = 0; r < nq && ok; ++r) {
-            const int s = (qs + r) & 1;
-            if (quse[s] > 0 && !mbar_wait(&bars->qempty[s], (quse[s] - 1) & 1u, FLAG_EMPTY_WAIT, c.abort_flag)) {
+            const int s = (k.qs + r) & 1;
+            const uint32_t use = s ? k.quse1 : k.quse0;
+            if (use > 1 && !mbar_wait(&bars->qempty[s], use & 1u, FLAG_EMPTY_WAIT, c.abort_flag)) {
                 ok = false;
                 break;
             }
@@ -221,9 +422,7 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
             for (int ch = 0; ch < C::NCH; ++ch)
                 tma_load_4d(c.smem + C::OFF_Q + s * C::Q_BYTES + ch * CHUNK, qm, &bars->qfull[s], 64 * ch, 0, pc.j, tok,
                             keep);
-            ++quse[s];
         }
-        if (!pc.two) qs ^= 1;
         // (the prefix is read again by the CTAs that serve its other row tiles)
         const CUtensorMap *km = pc.prefix ? kp : ks, *vm = pc.prefix ? vp : vs;
         const uint64_t pol = pc.prefix ? keep : once;
@@ -250,163 +449,239 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
         // Let every copy already issued land before the CTA can exit.
         for (uint32_t m = n > C::NS ? n - C::NS : 0; m < n; ++m)
             mbar_wait_sleep(&bars->full[m % C::NS], (m / C::NS) & 1u, FLAG_FULL_WAIT, nullptr);
-        for (int s = 0; s < 2; ++s)
-            if (quse[s] > 0) mbar_wait_sleep(&bars->qfull[s], (quse[s] - 1) & 1u, FLAG_FULL_WAIT, nullptr);
+        if (k.quse0 > 0) mbar_wait_sleep(&bars->qfull[0], (k.quse0 - 1) & 1u, FLAG_FULL_WAIT, nullptr);
+        if (k.quse1 > 0) mbar_wait_sleep(&bars->qfull[1], (k.quse1 - 1) & 1u, FLAG_FULL_WAIT, nullptr);
     }
 }
 
-// ------------------------------------------------------------------ MMA issuer (warp 1, lane 0)
-// A walk over the CTA's steps.
-struct Walk {
-    Piece pc;
-    long long pos;
-    int i;               // step within the piece
-    uint32_t tile;       // K/V tiles of the pieces before
-    int qs;              // Q slot of the piece's first row tile
-    uint32_t quse[2];    // pieces' uses of a Q slot, this one included
-    bool done;
-};
-__device__ __forceinline__ void walk_piece(Walk &k, const PrefixParams &p, const Ctx &c) {
-    if (k.pos >= c.p1) {
-        k.done = true;
-        return;
-    }
-    k.pc = next_piece(p, c.line, c.s_prefix, k.pos, c.p1, c.w);
-    k.i = 0;
-    ++k.quse[k.qs];
-    if (k.pc.two) ++k.quse[k.qs ^ 1];
-}
-__device__ __forceinline__ Walk walk_start(const PrefixParams &p, const Ctx &c) {
-    Walk k;
-    k.pos = c.p0;
-    k.tile = 0;
-    k.qs = 0;
-    k.quse[0] = k.quse[1] = 0;
-    k.done = false;
-    walk_piece(k, p, c);
-    return k;
-}
-__device__ __forceinline__ void walk_step(Walk &k, const PrefixParams &p, const Ctx &c) {
-    if (++k.i < k.pc.steps) return;
-    k.tile += k.pc.lt1 - k.pc.lt0;
-    if (!k.pc.two) k.qs ^= 1;
-    walk_piece(k, p, c);
-}
-
+// ------------------------------------------------------------------ MMA issuers (warps 1 and 2, lane 0)
+// Value product n of the group in two halves, then its score product n + 1: the latter overwrites
+// the weights that the former reads, and one thread's MMAs run in order.  The two issuers take
+// turns with the second half and the scores, in the order of the steps, so that one group's
+// products are queued together (a group whose next tiles have not landed gives its turn away
+// before the scores).
 template <int D>
-__device__ __forceinline__ void mma_issuer(const PrefixParams &p, const Ctx &c) {
+__device__ __forceinline__ void mma_issuer(const PrefixParams &p, const Ctx &c, int x) {
     using C = Cfg<D>;
     Bars *bars = c.bars;
-    const uint32_t tmem = bars->tmem;
     const uint32_t smem = smem_u32(c.smem);
+    const uint32_t ts = bars->tmem + TM_S + TM_X * x, to = bars->tmem + TM_O + TM_X * x;
     constexpr uint32_t idesc_qk = idesc_f16_major(128, TILE, 1, 1, 0, 0);
     constexpr uint32_t idesc_pv = idesc_f16_major(128, D, 1, 1, 0, 1);
-    uint32_t kseen = 0, vseen = 0;      // K / V tiles waited for
-
-    auto scores = [&](Walk &k, int x) -> bool {
-        const uint32_t t = k.tile + (uint32_t)(k.pc.two ? k.i >> 1 : k.i);
-        const uint32_t nk = 2 * t;
-        const int r = k.pc.two ? k.i & 1 : 0;
-        const int s = (k.qs + r) & 1;
-        if (!mbar_wait(&bars->qfull[s], (k.quse[s] - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return false;
-        if (kseen == t) {
-            if (!mbar_wait(&bars->full[nk % C::NS], (nk / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return false;
-            ++kseen;
+    Walk k = walk_start(c.line, c.w);
+    int i = 0, i0 = 0;                     // the step and the group's first step of the piece
+    auto next_piece = [&]() -> bool {      // to the next piece in which this group has a step
+        while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
+            i = i0 = (int)((k.steps & 1u) ^ (uint32_t)x);
+            if (i < k.pc.steps) return true;
         }
-        tc_fence_after();
-        const uint32_t q = smem + C::OFF_Q + s * C::Q_BYTES, kt = smem + (nk % C::NS) * C::KV_BYTES;
+        return false;
+    };
+    struct Step {
+        uint32_t nk, kslot, vslot, qpar;
+        int qslot, qoff;
+        bool first, last;
+    };
+    const int qoff_suffix = x == 1 ? suffix_shift(p.L * p.g) * 128 : 0;
+    auto step = [&]() -> Step {
+        Step s;
+        s.nk = 2 * (k.tiles + (uint32_t)(k.pc.two ? i >> 1 : i));
+        s.kslot = s.nk % C::NS;
+        s.vslot = (s.nk + 1) % C::NS;
+        s.qslot = k.pc.two ? (k.qs + i0) & 1 : k.qs;
+        s.qpar = ((s.qslot ? k.quse1 : k.quse0) - 1) & 1u;
+        s.qoff = k.pc.prefix ? 0 : qoff_suffix;
+        s.first = i == i0;
+        s.last = i + 2 >= k.pc.steps;
+        return s;
+    };
+    auto landed = [&](const Step &s) -> bool {
+        return (!s.first || mbar_test(&bars->qfull[s.qslot], s.qpar)) &&
+               mbar_test(&bars->full[s.kslot], (s.nk / C::NS) & 1u);
+    };
+    auto wait_landed = [&](const Step &s) -> bool {
+        if (s.first && !mbar_wait(&bars->qfull[s.qslot], s.qpar, FLAG_FULL_WAIT, c.abort_flag)) return false;
+        return mbar_wait(&bars->full[s.kslot], (s.nk / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag);
+    };
+    auto scores = [&](const Step &s) {
+        const uint32_t q = desc_lo(smem + C::OFF_Q + s.qslot * C::Q_BYTES - s.qoff, 16);
+        const uint32_t kt = desc_lo(smem + s.kslot * C::KV_BYTES, 16);
+        mma_ss<false>(ts, q, kt, idesc_qk);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
-            umma_ss(tmem + TM_S + TM_X * x, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(kt + off, 16, 1024),
-                    idesc_qk, kk ? 1u : 0u);
+        for (int kk = 1; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * CHUNK + (kk & 3) * 32) >> 4;
+            mma_ss<true>(ts, q + off, kt + off, idesc_qk);
         }
         umma_commit(&bars->sready[x]);
-        if (!k.pc.two || (k.i & 1)) umma_commit(&bars->empty[nk % C::NS]);
-        if (k.pc.two ? k.i >= k.pc.steps - 2 : k.i == k.pc.steps - 1) umma_commit(&bars->qempty[s]);
-        return true;
     };
-
-    Walk qk = walk_start(p, c), pv = qk;
-    uint32_t steps_x[2] = {0, 0};     // value products issued per group
-    uint32_t pieces_x[2] = {0, 0};    // pieces group x has taken part in
-    int xq = 0, xp = 0;
-    for (int i = 0; i < 2 && !qk.done; ++i, xq ^= 1) {
-        if (!scores(qk, xq)) return;
-        walk_step(qk, p, c);
-    }
-    while (!pv.done) {
-        const int x = xp;
-        const uint32_t t = pv.tile + (uint32_t)(pv.pc.two ? pv.i >> 1 : pv.i);
-        const uint32_t nv = 2 * t + 1;
-        const bool first = pv.i < 2, last = pv.i >= pv.pc.steps - 2;
-        if (!mbar_wait(&bars->pready[x], steps_x[x] & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-        if (vseen == t) {
-            if (!mbar_wait(&bars->full[nv % C::NS], (nv / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-            ++vseen;
-        }
-        if (first && pieces_x[x] > 0 &&
-            !mbar_wait(&bars->ofree[x], (pieces_x[x] - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag))
-            return;
+    if (!next_piece()) return;
+    Step cur = step();
+    if (!wait_landed(cur)) return;
+    tc_fence_after();
+    scores(cur);
+    uint32_t pieces = 0;                   // pieces whose last value product is issued
+    for (uint32_t n = 0;; ++n) {
+        bool more = true;
+        i += 2;
+        if (cur.last) more = next_piece();
+        Step nxt = cur;
+        if (more) nxt = step();
+        if (!mbar_wait(&bars->full[cur.vslot], ((cur.nk + 1) / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+        if (cur.first && pieces > 0 && !mbar_wait(&bars->ofree[x], (pieces - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+        if (!mbar_wait(&bars->pready[x][0], n & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
         tc_fence_after();
-        const uint32_t vt = smem + (nv % C::NS) * C::KV_BYTES;
+        const uint32_t vt = desc_lo(smem + cur.vslot * C::KV_BYTES, CHUNK);
+        if (cur.first) mma_ts<false>(to, ts, vt, idesc_pv);
+        else mma_ts<true>(to, ts, vt, idesc_pv);
 #pragma unroll
-        for (int kk = 0; kk < TILE / 16; ++kk)
-            umma_ts(tmem + TM_O + TM_X * x, tmem + TM_S + TM_X * x + kk * 8,
-                    smem_desc_sw128(vt + kk * 2048, CHUNK, 1024), idesc_pv, (!first || kk) ? 1u : 0u);
-        if (!pv.pc.two || (pv.i & 1)) umma_commit(&bars->empty[nv % C::NS]);
-        if (last) {
+        for (int kk = 1; kk < TILE / 32; ++kk) mma_ts<true>(to, ts + kk * 8, vt + kk * (2048 >> 4), idesc_pv);
+        if (!mbar_wait(&bars->pready[x][1], n & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+        const uint32_t turn = n - (x == 0 ? 1u : 0u);
+        if (turn != ~0u && !mbar_wait(&bars->turn[x], turn & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = TILE / 32; kk < TILE / 16; ++kk) mma_ts<true>(to, ts + kk * 8, vt + kk * (2048 >> 4), idesc_pv);
+        if (cur.last) {
             umma_commit(&bars->odone[x]);
-            ++pieces_x[x];
+            ++pieces;
         }
-        ++steps_x[x];
-        xp ^= 1;
-        walk_step(pv, p, c);
-        if (!qk.done) {
-            if (!scores(qk, xq)) return;
-            xq ^= 1;
-            walk_step(qk, p, c);
+        const bool now = more && landed(nxt);
+        if (now) {
+            tc_fence_after();
+            scores(nxt);
         }
+        mbar_arrive(&bars->turn[x ^ 1]);
+        if (!more) return;
+        if (!now) {
+            if (!wait_landed(nxt)) return;
+            tc_fence_after();
+            scores(nxt);
+        }
+        cur = nxt;
     }
 }
 
 // ------------------------------------------------------------------ softmax (warps 4..11)
+// 64 weights 2^(cs s - m) as bf16 pairs, and their sum.
+__device__ __forceinline__ float weights64(const float *s, float cs, float m, uint32_t (&w)[32]) {
+    const float off = m == -INFINITY ? 0.f : -m;
+    const uint64_t cs2 = pack2(cs, cs), off2 = pack2(off, off);
+    uint64_t l2[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        const uint64_t z = fma2(pack2(s[2 * e], s[2 * e + 1]), cs2, off2);
+        float a, b;
+        if (e % 8 < POLY) {
+            const uint64_t v = exp2_poly2(z);
+            l2[e & 1] = add2(l2[e & 1], v);
+            unpack2(v, a, b);
+        } else {
+            unpack2(z, a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            l2[e & 1] = add2(l2[e & 1], pack2(a, b));
+        }
+        w[e] = pack_bf16x2(a, b);
+    }
+    float la, lb;
+    unpack2(add2(l2[0], l2[1]), la, lb);
+    // (a row that has seen nothing yet has no sum: the polynomial's weights do not reach zero)
+    return m == -INFINITY ? 0.f : la + lb;
+}
+__device__ __forceinline__ float max128(const float *s) {
+    float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+#pragma unroll
+    for (int e = 4; e + 8 <= TILE; e += 8) {
+        t0 = max3(t0, s[e], s[e + 1]);
+        t1 = max3(t1, s[e + 2], s[e + 3]);
+        t2 = max3(t2, s[e + 4], s[e + 5]);
+        t3 = max3(t3, s[e + 6], s[e + 7]);
+    }
+    t0 = max3(t0, s[TILE - 4], s[TILE - 3]);
+    t1 = max3(t1, s[TILE - 2], s[TILE - 1]);
+    return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+}
+// O *= a (the columns of this thread's row).
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t to, float a) {
+#pragma unroll 1
+    for (int d = 0; d < D; d += 16) {
+        uint32_t o[16];
+        tmem_ld16(to + d, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+        tmem_st16(to + d, o);
+    }
+    tmem_wait_st();
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &c, int warp, int lane) {
+    using C = Cfg<D>;
     Bars *bars = c.bars;
     const uint32_t tmem = bars->tmem;
     const int x = (warp - 4) >> 2;
     const int quad = warp & 3;
-    const int r = 32 * quad + lane;                   // row of the tile
+    const int lrow = 32 * quad + lane;                // TMEM lane
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t ts = tmem + lanes + TM_S + TM_X * x, to = tmem + lanes + TM_O + TM_X * x;
     const bool negate = p.scale_log2 < 0.f;           // (the maximum is taken of the unscaled scores)
     const float cs = fmaxf(fabsf(p.scale_log2), 1e-30f);   // (a zero scale: masked scores stay -inf)
     uint32_t n_x = 0, pieces = 0;                     // steps and pieces of this group
-    uint32_t i0 = 0;                                  // steps of the pieces before
-    for (long long pos = c.p0; pos < c.p1;) {
-        const Piece pc = next_piece(p, c.line, c.s_prefix, pos, c.p1, c.w);
-        const int first = (int)((i0 & 1u) ^ (uint32_t)x);      // this group's first step of the piece
-        i0 += (uint32_t)pc.steps;
+    Walk k = walk_start(c.line, c.w);
+    const Piece &pc = k.pc;
+    while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
+        const int first = (int)((k.steps & 1u) ^ (uint32_t)x);      // this group's first step of the piece
         const int part = first;                       // row tile (two) or share of the K/V tiles
+        const uint32_t use = pc.two ? 1u : 2u;        // arrivals that free a tile: one of each group, or both from one
         // rows of the tile that are real
         int rows = p.L * p.g;
         if (pc.prefix) {
             const int tok0 = (2 * pc.pair + (pc.two ? part : 0)) * p.tok_tile;
             rows = min(p.tok_tile, p.B * p.L - tok0) * p.g;
         }
-        const bool warp_on = 32 * quad < rows;
+        // row of the tile (suffixes: group 1's lie further up)
+        const int r = lrow - (!pc.prefix && x == 1 ? suffix_shift(rows) : 0);
+        const int q_on = r - lane;                    // the warp's first row
+        const bool warp_on = q_on >= 0 && q_on < rows;
+        // the suffixes come last and all have as many rows: warps without any are done, and the
+        // first answers for them
+        if (!pc.prefix && !warp_on) return;
+        const bool releases = lane == 0 && q_on == 0;
+        const uint32_t arrivals = pc.prefix || q_on > 0 ? 1u : 4u - (uint32_t)((rows - 1) / 32);
         // positions this row sees: all of the prefix; a suffix up to its own token
         const int limit = pc.prefix ? pc.len : pc.len - p.L + 1 + min(r / p.g, p.L - 1);
         float m = -INFINITY, l = 0.f;                 // (log2 units; m in scaled scores)
+        float m_next = -INFINITY;                     // the maximum from the next step on
         for (int i = first; i < pc.steps; i += 2, ++n_x) {
-            const int lt = pc.lt0 + (pc.two ? i >> 1 : i);
+            const int it = pc.two ? i >> 1 : i;
             if (!warp_all(mbar_wait(&bars->sready[x], n_x & 1u, FLAG_MMA_WAIT, c.abort_flag))) return;
+            // the scores are there: this group is done with the K tile, with the V tile of its step
+            // before, and after its last step with Q
+            if (releases) {
+                const uint32_t nk = 2 * (k.tiles + (uint32_t)it);
+                mbar_arrive_n(&bars->empty[nk % C::NS], use);
+                if (i != first) {
+                    const uint32_t nv = nk + 1 - (pc.two ? 2u : 4u);
+                    mbar_arrive_n(&bars->empty[nv % C::NS], use);
+                }
+                if (i + 2 >= pc.steps)
+                    mbar_arrive_n(&bars->qempty[pc.two ? (k.qs + first) & 1 : k.qs], pc.two || pc.steps == 1 ? 2u : 1u);
+            }
+            float s[TILE];
+            uint32_t w[32];
             if (warp_on) {
                 tc_fence_after();
-                float s[TILE];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * h));
+                // O_x is complete up to the last step (its product precedes these scores)
+                if (__any_sync(0xffffffffu, m_next != m)) {
+                    const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_next);
+                    l *= a;
+                    rescale<D>(to, a);
+                    m = m_next;
+                }
                 tmem_wait_ld();
                 if (negate) {
 #pragma unroll
@@ -414,98 +689,90 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
                 }
                 // the tile's first position (a unit's last tile ends at its length: its first
                 // columns repeat earlier positions, or lie before the cache)
-                const int tok0 = lt * TILE;
+                const int tok0 = (pc.lt0 + it) * TILE;
                 const int y = min(tok0, pc.len - TILE);
-                const bool masked = y < tok0 || (!pc.prefix && tok0 + TILE > pc.len - p.L + 1);
-                if (masked) {
+                if (y < tok0 || (!pc.prefix && tok0 + TILE > pc.len - p.L + 1)) {
                     const int lo = tok0 - y, hi = limit - y;
 #pragma unroll
                     for (int e = 0; e < TILE; ++e) s[e] = (e >= lo && e < hi) ? s[e] : -INFINITY;
                 }
-                float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
-#pragma unroll
-                for (int e = 4; e < TILE; e += 4) {
-                    t0 = fmaxf(t0, s[e]);
-                    t1 = fmaxf(t1, s[e + 1]);
-                    t2 = fmaxf(t2, s[e + 2]);
-                    t3 = fmaxf(t3, s[e + 3]);
-                }
-                const float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * cs;
-                const bool move = tm > m + RESCALE || (m == -INFINITY && tm > m);
-                const float m_new = move ? tm : m;
-                if (__any_sync(0xffffffffu, move && m != -INFINITY)) {
-                    // O_x up to the last step is complete (its product precedes these scores)
-                    const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_new);
-                    l *= a;
-#pragma unroll 1
-                    for (int h = 0; h < D; h += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + h, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tmem_st32(to + h, o);
+                if (i == first) m = m_next = max128(s) * cs;
+                float lsum = weights64(s, cs, m, w);
+                const float tm = max128(s) * cs;
+                if (__any_sync(0xffffffffu, tm > m + LIMIT)) {
+                    const float m_new = fmaxf(m, tm);
+                    if (i != first) {
+                        const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_new);
+                        l *= a;
+                        rescale<D>(to, a);
                     }
-                    tmem_wait_st();
+                    m = m_new;
+                    lsum = weights64(s, cs, m, w);
                 }
-                m = m_new;
-                const float off = m == -INFINITY ? 0.f : -m;
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float a = fast_exp2(fmaf(s[64 * h + 2 * e], cs, off));
-                        const float b = fast_exp2(fmaf(s[64 * h + 2 * e + 1], cs, off));
-                        l0 += a;
-                        l1 += b;
-                        w[e] = pack_bf16x2(a, b);
-                    }
-                    tmem_st32(ts + 32 * h, w);
-                }
-                l += l0 + l1;
+                m_next = tm > m + RESCALE ? tm : m;
+                l += lsum;
+                tmem_st32(ts, w);
                 tmem_wait_st();
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->pready[x]);
+            if (lane == 0) mbar_arrive_n(&bars->pready[x][0], arrivals);
+            if (warp_on) {
+                l += weights64(s + 64, cs, m, w);
+                tmem_st32(ts + 32, w);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(&bars->pready[x][1], arrivals);
         }
         // ---- the piece's partial: O / l and log2 of the sum
-        if (first < pc.steps) {
+        const bool took = first < pc.steps;
+        if (took) {
             if (!warp_all(mbar_wait(&bars->odone[x], pieces & 1u, FLAG_MMA_WAIT, c.abort_flag))) return;
             ++pieces;
             tc_fence_after();
+            if (releases) {
+                const int last = first + ((pc.steps - 1 - first) & ~1);
+                const uint32_t nv = 2 * (k.tiles + (uint32_t)(pc.two ? last >> 1 : last)) + 1;
+                mbar_arrive_n(&bars->empty[nv % C::NS], use);
+            }
         }
         if (warp_on) {
             const bool on = r < rows;
             // (a NaN sum stays NaN)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
-            const int nr = pc.prefix ? ROWS : p.L * p.g;
-            const size_t at = ((size_t)pc.slot * 2 + part) * nr + r;
-            if (on) (pc.prefix ? p.lse_p : p.lse_s)[at] = lse2;
-            if (first < pc.steps) {
-                float *dst = (pc.prefix ? p.o_p : p.o_s) + at * D;
-#pragma unroll 1
-                for (int h = 0; h < D; h += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + h, o);
-                    tmem_wait_ld();
-                    if (on) {
+            const size_t at = (size_t)pc.slot * 2 + part;
+            const uint32_t rs = (uint32_t)(p.L * p.g);
+            if (on) {
+                if (pc.prefix) p.lse_p[at * ROWS + r] = lse2;
+                else p.lse_s[at * rs + r] = lse2;
+            }
+            if (took) {
+                // prefix rows next to each other, so that a warp stores whole lines; a suffix's few
+                // rows each by itself
+                float *dst = pc.prefix ? p.o_p + at * D * ROWS + r : p.o_s + (at * rs + r) * D;
+                uint32_t o[D];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + h + e) =
-                                make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                            __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                    }
+                for (int d = 0; d < D; d += 32) tmem_ld32(to + d, *reinterpret_cast<uint32_t(*)[32]>(o + d));
+                tmem_wait_ld();
+                if (on && pc.prefix) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d) dst[d * ROWS] = __uint_as_float(o[d]) * inv;
+                } else if (on) {
+#pragma unroll
+                    for (int d = 0; d < D; d += 4)
+                        *reinterpret_cast<float4 *>(dst + d) =
+                            make_float4(__uint_as_float(o[d]) * inv, __uint_as_float(o[d + 1]) * inv,
+                                        __uint_as_float(o[d + 2]) * inv, __uint_as_float(o[d + 3]) * inv);
                 }
                 tc_fence_before();
             }
         }
-        if (first < pc.steps) {
+        if (took) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->ofree[x]);
+            if (lane == 0) mbar_arrive_n(&bars->ofree[x], arrivals);
         }
     }
 }
@@ -519,34 +786,37 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
                      const __grid_constant__ CUtensorMap qm) {
     using namespace pfx;
     using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t prefix_smem[];
+    uint8_t *smem = prefix_smem;
     Bars *bars = reinterpret_cast<Bars *>(smem + C::OFF_BARS);
-    int *pub = reinterpret_cast<int *>(p.meta + 2);
-    int *s_prefix = p.prefix_in_ws ? pub : reinterpret_cast<int *>(smem + C::OFF_PREFIX);
+    uint32_t *pub = p.meta + 2;
+    uint32_t *tab = p.table_in_ws ? pub : reinterpret_cast<uint32_t *>(smem + C::OFF_TABLE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int s = 0; s < C::NS; ++s) {
+        for (uint32_t s = 0; s < C::NS; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->empty[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->qfull[i], 1);
-            mbar_init(&bars->qempty[i], 1);
+            mbar_init(&bars->qempty[i], 2);
             mbar_init(&bars->sready[i], 1);
-            mbar_init(&bars->pready[i], 4);
+            mbar_init(&bars->pready[i][0], 4);
+            mbar_init(&bars->pready[i][1], 4);
+            mbar_init(&bars->turn[i], 1);
             mbar_init(&bars->odone[i], 1);
             mbar_init(&bars->ofree[i], 4);
         }
         bars->abort_flag = 0;
         fence_mbar_init();
     }
+    if (tid == 32 * 2) bars->prefix_len = clamp_len(__ldg(p.prefix_len), p.P_max);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem), 512);
         tmem_relinquish();
     }
-    if (warp == 2 && !p.prefix_in_ws) build_tile_prefix(p.seq_lens, p.B, p.T_max, TILE, s_prefix, lane);
-    if (warp == 0 && lane == 0) {
+    if (warp == 3 && !p.table_in_ws) build_table(p.seq_lens, p.B, p.T_max, tab, lane);
+    if (warp == 0 && lane == 1) {
         prefetch_tensormap(&kp);
         prefetch_tensormap(&vp);
         prefetch_tensormap(&ks);
@@ -561,31 +831,25 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
     c.smem = smem;
     c.bars = bars;
     c.abort_flag = &bars->abort_flag;
-    c.s_prefix = s_prefix;
-    c.line = make_line(p, s_prefix[p.B]);
+    c.tab = tab;
+    c.prefix_len = bars->prefix_len;
+    c.line = make_line(p, (uint32_t)tiles_of(c.prefix_len, TILE), table_units(tab[p.B]));
     c.w = blockIdx.x;
-    c.p0 = (long long)blockIdx.x * c.line.W;
-    c.p1 = c.p0 + c.line.W < c.line.total ? c.p0 + c.line.W : c.line.total;
-    if (blockIdx.x == 0) {
-        if (tid == 0) {
-            p.meta[0] = c.line.n_p;
-            p.meta[1] = c.line.W;
-        }
-        if (!p.prefix_in_ws)
-            for (int i = tid; i <= p.B; i += NTHREADS) pub[i] = s_prefix[i];
+    if (blockIdx.x == 0 && warp == 3) {
+        if (lane == 0) p.meta[0] = c.line.n_p;
+        if (!p.table_in_ws)
+            for (int i = lane; i <= p.B; i += 32) pub[i] = tab[i];
     }
     // The merge kernel may be scheduled now; it waits for this grid to finish.
     pdl_launch_dependents();
 
     if (warp < 4) {
         regs_dec<REGS_CTRL>();
-        if (c.p0 < c.p1) {
-            if (warp == 0 && lane == 0) producer<D>(p, &kp, &vp, &ks, &vs, &qm, c);
-            if (warp == 1 && lane == 0) mma_issuer<D>(p, c);
-        }
+        if (warp == 0 && lane == 0) producer<D>(p, &kp, &vp, &ks, &vs, &qm, c);
+        if ((warp == 1 || warp == 2) && lane == 0) mma_issuer<D>(p, c, warp - 1);
     } else {
         regs_inc<REGS_SOFT>();
-        if (c.p0 < c.p1) softmax_group<D>(p, c, warp, lane);
+        softmax_group<D>(p, c, warp, lane);
     }
     __syncwarp();
     tc_fence_before();
@@ -596,98 +860,118 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
     }
 }
 
-// The suffix tile prefix of a batch too large for the decode kernel's shared memory.
-__global__ void __launch_bounds__(32) prefix_tiles_kernel(const PrefixParams p) {
-    build_tile_prefix(p.seq_lens, p.B, p.T_max, pfx::TILE, reinterpret_cast<int *>(p.meta + 2), threadIdx.x);
+// The suffix table of a batch too large for the decode kernel's shared memory.
+__global__ void __launch_bounds__(32) prefix_table_kernel(const PrefixParams p) {
+    pfx::build_table(p.seq_lens, p.B, p.T_max, p.meta + 2, threadIdx.x);
 }
 
-// Joins a row's partials: one warp per (new token, query head), its lanes across the head
-// dimension.  The partials lie in L2 (they were just written); the loads of eight are in flight.
+// Joins the rows' partials.  A CTA takes 32 rows of a row tile, a lane each (the partials lie
+// row by row), and 32 dimensions, four a warp.  The log-sum-exps of up to 64 partials are
+// gathered first; the loads of their values then depend on nothing and are in flight together.
+// The result goes through shared memory to be written in whole rows.
+constexpr int kMergeWarps = 8, kMergeChunk = 64;
 template <int D>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixParams p) {
     using namespace pfx;
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);     // ((b * L + qi) * n_q + h)
-    if (row >= (long long)p.B * p.L * p.n_q) return;
-    const int h = (int)(row % p.n_q), tok = (int)(row / p.n_q);
-    const int j = h / p.g, hg = h % p.g, b = tok / p.L, qi = tok % p.L;
-    const int rt = tok / p.tok_tile, pr = (tok % p.tok_tile) * p.g + hg;      // row tile, row in it
-    const long long u = (long long)j * p.pairs + rt / 2;
+    constexpr int V = 32 / kMergeWarps;
+    __shared__ float s_lse[kMergeChunk][32];
+    __shared__ float s_out[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // block -> (KV head, row tile, quarter)
+    const int quarter = blockIdx.x & 3, rt = (blockIdx.x >> 2) % p.row_tiles, j = (blockIdx.x >> 2) / p.row_tiles;
+    const int pr = 32 * quarter + lane;
+    const int tok = rt * p.tok_tile + pr / p.g, hg = pr % p.g;
+    const bool on = pr < p.tok_tile * p.g && tok < p.B * p.L;
+    if (__syncthreads_or(on) == 0) return;
+    const int b = on ? tok / p.L : 0, qi = on ? tok % p.L : 0;
+    const uint32_t u = (uint32_t)(j * p.pairs + rt / 2);
     const bool two = (rt | 1) < p.row_tiles;
+    const uint32_t rs = (uint32_t)(p.L * p.g), sr = (uint32_t)(qi * p.g + hg);
 
     pdl_wait_primary();
-    const int n_p = (int)p.meta[0];
-    const long long W = p.meta[1];
-    const int *pre = reinterpret_cast<const int *>(p.meta + 2);
-    const int wp = p.row_tiles > 1 ? 2 : 1;
-    const long long p_total = (long long)p.n_kv * p.pairs * n_p * wp;
-    // prefix partials: workers [w0, w1], one part each (two row tiles) or two
-    const long long ua = u * n_p * wp, ub = ua + (long long)n_p * wp;
-    const int w0 = n_p > 0 ? (int)(ua / W) : 0, w1 = n_p > 0 ? (int)((ub - 1) / W) : -1;
-    const int np = (w1 - w0 + 1) * (two ? 1 : 2);
-    // suffix partials: workers [v0, v1], two parts each
-    const int nt = pre[b + 1] - pre[b];
-    const long long sa = p_total + (long long)pre[b] * p.n_kv + (long long)j * nt;
-    const int v0 = nt > 0 ? (int)(sa / W) : 0, v1 = nt > 0 ? (int)((sa + nt - 1) / W) : -1;
-    const int ns = (v1 - v0 + 1) * 2;
-    const int rs = p.L * p.g, sr = qi * p.g + hg;
+    const uint32_t *tab = p.meta + 2;
+    const Line l = make_line(p, p.meta[0], table_units(tab[p.B]));
+    // prefix partials: workers w0 .. w1, one part each (two row tiles) or two
+    const uint32_t ua = u * l.unit_p;
+    const int w0 = (int)(ua / l.W), w1 = l.n_p > 0 ? (int)((ua + l.unit_p - 1) / l.W) : w0 - 1;
+    const int sh = two ? 0 : 1, part0 = two ? rt & 1 : 0;
+    const int np = (w1 - w0 + 1) << sh;
+    // suffix partials: workers v0 .. v1, two parts each
+    const uint32_t cu = on ? table_units(tab[b + 1]) - table_units(tab[b]) : 0;
+    const uint32_t sa = l.p_total + (table_units(tab[b]) * (uint32_t)p.n_kv + (uint32_t)j * cu) * WS;
+    const int v0 = (int)(sa / l.W), v1 = cu > 0 ? (int)((sa + cu * WS - 1) / l.W) : v0 - 1;
+    const int n = np + __reduce_max_sync(0xffffffffu, (v1 - v0 + 1) * 2);
+    const uint32_t at_p = (u + (uint32_t)w0) * 2 + (uint32_t)part0;      // partial i < np: at_p + (two ? 2 i : i)
+    const uint32_t at_s = (uint32_t)(b * p.n_kv + j + v0) * 2;           // partial np + i: at_s + i
 
     float m = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    constexpr int U = 8;
-    for (int k0 = 0; k0 < np + ns; k0 += U) {
-        float ls[U], o[U][V];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
+    const int d0 = 32 * blockIdx.y + warp * V;
+    for (int k0 = 0; k0 < n; k0 += kMergeChunk) {
+        const int kn = min(kMergeChunk, n - k0);
+        if (k0 > 0) __syncthreads();
+        for (int k = warp; k < kn; k += kMergeWarps) {
             const int i = k0 + k;
-            ls[k] = -INFINITY;
-            const float *src = nullptr;
+            float x = -INFINITY;       // no such partial, or nothing seen in it
+            uint32_t a, z;
             if (i < np) {
-                const int w = two ? i : i >> 1, part = two ? rt & 1 : i & 1;
-                const size_t at = ((size_t)(u + w0 + w) * 2 + part) * ROWS + pr;
-                ls[k] = p.lse_p[at];
-                src = p.o_p + at * D;
-            } else if (i < np + ns) {
-                const int w = (i - np) >> 1, part = (i - np) & 1;
-                const size_t at = ((size_t)((long long)b * p.n_kv + j + v0 + w) * 2 + part) * rs + sr;
-                ls[k] = p.lse_s[at];
-                src = p.o_s + at * D;
+                prefix_piece(l, ua, (uint32_t)(w0 + (i >> sh)), a, z);
+                if (on && a < z) x = p.lse_p[(size_t)(at_p + (two ? 2 * i : i)) * ROWS + pr];
+            } else if (v0 + ((i - np) >> 1) <= v1) {
+                suffix_piece(l, sa, cu - 1, (uint32_t)(v0 + ((i - np) >> 1)), a, z);
+                if (a < z) x = p.lse_s[(size_t)(at_s + (i - np)) * rs + sr];
             }
+            s_lse[k][lane] = x;
+        }
+        __syncthreads();
+        float mc = m;
+        for (int k = 0; k < kn; ++k) {
+            const float x = s_lse[k][lane];
+            mc = x > mc || x != x ? x : mc;      // (NaN stays)
+        }
+        const float off = mc == -INFINITY ? 0.f : mc;
+        const float scale = fast_exp2(m - off);
+        sum *= scale;
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[k][v] = 0.f;
-            if (src != nullptr) {
-                if constexpr (V == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src + lane * 4);
-                    o[k][0] = f.x; o[k][1] = f.y; o[k][2] = f.z; o[k][3] = f.w;
+        for (int v = 0; v < V; ++v) acc[v] *= scale;
+        m = mc;
+#pragma unroll 8
+        for (int k = 0; k < kn; ++k) {
+            const int i = k0 + k;
+            const float x = s_lse[k][lane];
+            const float w = fast_exp2(x - off);
+            const bool pre = i < np;
+            float f[V] = {};
+            if (x != -INFINITY) {
+                if (pre) {
+                    const float *o = p.o_p + ((size_t)(at_p + (two ? 2 * i : i)) * D + d0) * ROWS + pr;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) f[v] = o[v * ROWS];
                 } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(src + lane * 2);
-                    o[k][0] = f.x; o[k][1] = f.y;
+                    const float4 o = *reinterpret_cast<const float4 *>(p.o_s + ((size_t)(at_s + (i - np)) * rs + sr) * D + d0);
+                    f[0] = o.x; f[1] = o.y; f[2] = o.z; f[3] = o.w;
                 }
             }
-        }
+            sum += w;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (ls[k] == -INFINITY) continue;      // nothing seen there (its values are not read)
-            const float mn = fmaxf(m, ls[k]);
-            const float a = fast_exp2(m - mn), w = fast_exp2(ls[k] - mn);
-            sum = sum * a + w;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = acc[v] * a + w * o[k][v];
-            m = mn;
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, f[v], acc[v]);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t packed[V / 2];
 #pragma unroll
-    for (int v = 0; v < V; v += 2) packed[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
-    __nv_bfloat16 *dst = p.out + row * D + lane * V;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(packed[0], packed[1]);
-    else
-        *reinterpret_cast<uint32_t *>(dst) = packed[0];
-    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
+    for (int v = 0; v < V; ++v) s_out[lane][warp * V + v] = acc[v] * inv;
+    if (blockIdx.y == 0 && warp == 0 && on)
+        p.lse[(size_t)tok * p.n_q + j * p.g + hg] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
+    __syncthreads();
+    // four bf16 a thread, eight threads a row
+    const int rr = threadIdx.x >> 3, c4 = (threadIdx.x & 7) * 4;
+    const int q = 32 * quarter + rr, t = rt * p.tok_tile + q / p.g;
+    if (q < p.tok_tile * p.g && t < p.B * p.L) {
+        const float *s = &s_out[rr][c4];
+        *reinterpret_cast<uint2 *>(p.out + ((size_t)t * p.n_q + j * p.g + q % p.g) * D + 32 * blockIdx.y + c4) =
+            make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    }
 }
 
 }  // namespace kvattn

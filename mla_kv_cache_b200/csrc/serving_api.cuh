@@ -21,11 +21,11 @@ int launch_prefix(PrefixParams &p, const CUtensorMap *maps, DeviceState *dev, cu
     auto kern = prefix_decode_kernel<D>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), dev, C::SMEM);
     if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(prefix decode)");
-    p.prefix_in_ws = p.B > C::B_SMEM;
-    if (p.prefix_in_ws) {
-        prefix_tiles_kernel<<<1, 32, 0, s>>>(p);
+    p.table_in_ws = p.B > C::B_SMEM;
+    if (p.table_in_ws) {
+        prefix_table_kernel<<<1, 32, 0, s>>>(p);
         e = cudaGetLastError();
-        if (e != cudaSuccess) return fail_cuda(e, "prefix tiles launch");
+        if (e != cudaSuccess) return fail_cuda(e, "prefix table launch");
         ++t_launches;
     }
     kern<<<p.workers, pfx::NTHREADS, C::SMEM, s>>>(p, maps[0], maps[1], maps[2], maps[3], maps[4]);
@@ -36,9 +36,8 @@ int launch_prefix(PrefixParams &p, const CUtensorMap *maps, DeviceState *dev, cu
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const long long rows = (long long)p.B * p.L * p.n_q;
-    cfg.gridDim = dim3((unsigned)((rows + 3) / 4), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.gridDim = dim3((unsigned)(4 * p.row_tiles * p.n_kv), D / 32, 1);
+    cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -52,6 +51,7 @@ int launch_prefix(PrefixParams &p, const CUtensorMap *maps, DeviceState *dev, cu
 struct PrefixPlan {
     int tok_tile, row_tiles, pairs, workers;
     size_t meta, lse_p, lse_s, o_p, o_s, bytes;   // byte offsets, total
+    long long line;                               // positions of the full capacity
 };
 PrefixPlan prefix_plan(const DeviceState *dev, int B, int L, int n_q, int n_kv, int D, int P_max, int T_max) {
     PrefixPlan w;
@@ -61,16 +61,16 @@ PrefixPlan prefix_plan(const DeviceState *dev, int B, int L, int n_q, int n_kv, 
     w.pairs = (w.row_tiles + 1) / 2;
     const long long tiles_p = (P_max + pfx::TILE - 1) / pfx::TILE, tiles_s = (T_max + pfx::TILE - 1) / pfx::TILE;
     const long long units_p = (long long)n_kv * w.pairs, units_s = (long long)B * n_kv;
-    const long long line = units_p * tiles_p * (w.row_tiles > 1 ? 2 : 1) + units_s * tiles_s;
+    w.line = units_p * tiles_p * (w.row_tiles > 1 ? pfx::WP2 : pfx::WP1) + units_s * (tiles_s + 1) * pfx::WS;
     long long workers = g_force_workers > 0 ? g_force_workers : dev->sms;
-    const long long most = (line + pfx::MIN_TILES - 1) / pfx::MIN_TILES;
+    const long long most = (w.line + pfx::W_MIN - 1) / pfx::W_MIN;
     if (workers > most) workers = most;
     if (workers < 1) workers = 1;
     w.workers = (int)workers;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t rows_p = (size_t)(units_p + workers) * 2 * pfx::ROWS, rows_s = (size_t)(units_s + workers) * 2 * L * g;
     w.meta = 0;
-    w.lse_p = up(16 + (size_t)(B + 1) * 4);
+    w.lse_p = up(8 + (size_t)(B + 1) * 4);
     w.lse_s = w.lse_p + up(rows_p * 4);
     w.o_p = w.lse_s + up(rows_s * 4);
     w.o_s = w.o_p + up(rows_p * D * 4);
@@ -119,6 +119,10 @@ int prefix_entry(const uint16_t *q, const uint16_t *kp, const uint16_t *vp, cons
     int st = device_state(&dev);
     if (st != KVATTN_OK) return st;
     const PrefixPlan w = prefix_plan(dev, batch, q_len, n_q, n_kv, d, max_prefix_len, max_seq_len);
+    if (w.line >= pfx::LINE_LIMIT) {
+        snprintf(t_detail, sizeof(t_detail), "prefix and caches hold more tiles than the work split counts");
+        return KVATTN_ERR_UNSUPPORTED;
+    }
     if (workspace_bytes < w.bytes) {
         snprintf(t_detail, sizeof(t_detail), "workspace of %zu B, %zu needed", workspace_bytes, w.bytes);
         return KVATTN_ERR_INVALID_ARG;
@@ -143,7 +147,7 @@ int prefix_entry(const uint16_t *q, const uint16_t *kp, const uint16_t *vp, cons
     p.out = reinterpret_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     char *ws = static_cast<char *>(workspace);
-    p.meta = reinterpret_cast<long long *>(ws + w.meta);
+    p.meta = reinterpret_cast<uint32_t *>(ws + w.meta);
     p.lse_p = reinterpret_cast<float *>(ws + w.lse_p);
     p.lse_s = reinterpret_cast<float *>(ws + w.lse_s);
     p.o_p = reinterpret_cast<float *>(ws + w.o_p);
