@@ -29,137 +29,179 @@ struct RowAppendParams {
     long long q_stride, q_out_stride, k_stride, v_stride;
     int N, n_q, n_kv, d, page_size;
     long long n_slots;             // num_pages * page_size
-    double log2_base;              // rotation base, log2
+    double turn_lo[16], turn_hi[8];   // turns per position of pair 16 h + l: turn_hi[h] * turn_lo[l]
     int rotate, interleaved;
-    int rows_per_cta;              // rows (heads of q, then k, then v) of a token one CTA takes
+    int parts, rows_per_part;      // a token's rows (heads of q, then k, then v) are shared out over warps
 };
 
 constexpr int kRowThreads = 128;
-constexpr int kRowMaxPairs = 128;  // head_dim <= 256
 
 // cos and sin of position * base^(-2i/d) for pair i.  The angle is formed in turns in fp64
 // (a position of 10^6 leaves it good to ~1e-10 of a turn) and only its fraction of a turn is
 // taken to fp32, so no reduction of a large argument is left to the fp32 functions; their
-// results are off by ~2e-7 at most, against 2^-9 of the bf16 rounding and 2^-4 of E4M3.
-__device__ __forceinline__ float2 rope_turn(int pos, int i, int d, double log2_base) {
-    const double turns = (double)pos * (exp2(-2.0 * (double)i / (double)d * log2_base) * 0.15915494309189533577);
+// results are off by ~2e-7 at most, against 2^-9 of the bf16 rounding and 2^-4 of E4M3.  A pair's
+// turns per position are a product of two of the 24 powers that come with the launch.
+__device__ __forceinline__ float2 rope_turn(const RowAppendParams &p, int pos, int i) {
+    const double turns = (double)pos * (p.turn_hi[i >> 4] * p.turn_lo[i & 15]);
     const float f = (float)(turns - rint(turns));
     float s, c;
     sincospif(2.f * f, &s, &c);
     return make_float2(c, s);
 }
 
-// One CTA per token (or per part of a token's rows when there are few tokens); LPR lanes of
-// eight elements make a row.  The rows' loads go out before the token's cos / sin table is
-// formed, so the fp64 work hides behind them.
-// Bound by memory: the new rows are read once (a fused projection's slices in place), the codes
-// and scales written once.
-template <int LPR>
-__global__ void __launch_bounds__(kRowThreads) row_append_kernel(const RowAppendParams p) {
-    __shared__ float2 s_turn[kRowMaxPairs];
-    constexpr int RPC = kRowThreads / LPR;       // rows the CTA handles at once
-    constexpr int U = 4;                         // of these per thread in flight
-    const int n = blockIdx.x;
-    const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
-    const int n_rows = p.n_q + 2 * p.n_kv;
-    const int r0 = blockIdx.y * p.rows_per_cta;
-    const int r1 = min(r0 + p.rows_per_cta, n_rows);
-    const bool lane_on = l * 8 < p.d;
-    const long long slot = __ldg(p.slots + n);
-    const bool store = slot >= 0 && slot < p.n_slots;
-    const int page = store ? (int)(slot / p.page_size) : 0;
-    const int prow = store ? (int)(slot - (long long)page * p.page_size) : 0;
+// Sixteen elements of a row: 8 at `at` and 8 half a row further.
+struct RowHalves {
+    uint4 lo, hi;
+};
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&y)[8]) {
+    y[0] = bf16_lo(v.x); y[1] = bf16_hi(v.x); y[2] = bf16_lo(v.y); y[3] = bf16_hi(v.y);
+    y[4] = bf16_lo(v.z); y[5] = bf16_hi(v.z); y[6] = bf16_lo(v.w); y[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+}
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+    uint32_t c[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const uint16_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * t] * inv, y[4 * t + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint16_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * t + 2] * inv, y[4 * t + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        c[t] = (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+    return make_uint2(c[0], c[1]);
+}
 
-    auto source = [&](int r) -> const uint4 * {
-        const __nv_bfloat16 *row;
-        if (r < p.n_q) row = p.q + (long long)n * p.q_stride + (long long)r * p.d;
-        else if (r < p.n_q + p.n_kv) row = p.k_new + (long long)n * p.k_stride + (long long)(r - p.n_q) * p.d;
-        else row = p.v_new + (long long)n * p.v_stride + (long long)(r - p.n_q - p.n_kv) * p.d;
-        return reinterpret_cast<const uint4 *>(row + l * 8);
+// A warp takes a token (or a part of its rows where there are few tokens); LPR lanes make a row,
+// a lane the elements i .. i + 7 of each half, so that both elements of every pair are its own,
+// in either pairing, and its eight cosines and sines serve all rows of the token from registers.
+// Bound by memory at best (the new rows are read once, a fused projection's slices in place; the
+// codes and scales written once) and by instructions next: a form with one vector a lane, its
+// partner by shuffles and the cosines in shared memory took 65 us for 8192 tokens of 64 + 2 * 8
+// heads of 128 (floor 49).
+template <int LPR>
+__global__ void __launch_bounds__(kRowThreads) row_append_kernel(const __grid_constant__ RowAppendParams p) {
+    constexpr int RPW = 32 / LPR;                // rows the warp handles at once
+    constexpr int U = 1;                         // of these in flight (more cost registers: 18.1 us with 2 for
+                                                 // 8192 tokens of 8 + 2 * 8 heads of 64, 14.1 with 1)
+    const int lane = threadIdx.x & 31;
+    const long long item = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int n = (int)(item / p.parts), part = (int)(item - (long long)n * p.parts);
+    if (n >= p.N) return;
+    const int sub = lane / LPR, l = lane % LPR;
+    const int n_rows = p.n_q + 2 * p.n_kv, half = p.d >> 1;
+    const int r0 = part * p.rows_per_part, r1 = min(r0 + p.rows_per_part, n_rows);
+    const bool lane_on = l * 8 < half;
+    const int at = lane_on ? l * 8 : 0;
+    const long long slot = __ldg(p.slots + n);
+
+    auto load = [&](const __nv_bfloat16 *row) -> RowHalves {
+        // (plain loads: the queries may be written in place)
+        RowHalves x;
+        x.lo = *reinterpret_cast<const uint4 *>(row + at);
+        x.hi = *reinterpret_cast<const uint4 *>(row + half + at);
+        return x;
     };
-    bool have_table = !p.rotate;
-    for (int base = r0; base < r1; base += RPC * U) {
-        uint4 x[U];
+    // pairs of this lane: at + t (split halves); at / 2 + t and half / 2 + at / 2 + t (interleaved)
+    float c[8], s[8];
+    if (p.rotate && r0 < p.n_q + p.n_kv) {
+        const int pos = __ldg(p.positions + n);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = base + u * RPC + sub;
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < r1 && lane_on && (r < p.n_q || store)) x[u] = *source(r);
+        for (int t = 0; t < 8; ++t) {
+            const int i = p.interleaved ? (at >> 1) + (t & 3) + (t >= 4 ? half >> 1 : 0) : at + t;
+            const float2 cs = rope_turn(p, pos, i);
+            c[t] = cs.x;
+            s[t] = cs.y;
         }
-        if (!have_table) {       // (uniform over the CTA)
-            const int pos = __ldg(p.positions + n);
-            for (int i = threadIdx.x; i < p.d / 2; i += kRowThreads) s_turn[i] = rope_turn(pos, i, p.d, p.log2_base);
-            __syncthreads();
-            have_table = true;
-        }
+    }
+    auto turn = [&](float (&a)[8], float (&b)[8]) {
+        if (p.interleaved) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = base + u * RPC + sub;
-            const bool row_on = r < r1 && (r < p.n_q || store);
-            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float y[8];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) { y[2 * t] = bf16_lo(w[t]); y[2 * t + 1] = bf16_hi(w[t]); }
-            // the other half's row elements (split halves): lanes d / 16 apart.  Every lane of
-            // the warp takes part in the exchange, whatever its row.
-            const int half = p.d / 16;
-            uint32_t o[4];
-            if (p.rotate && !p.interleaved) {
-                const int src = l < half ? l + half : l - half;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) o[t] = __shfl_sync(0xffffffffu, w[t], src & (LPR - 1), LPR);
+            for (int t = 0; t < 4; ++t) {
+                const float x = a[2 * t], y = a[2 * t + 1], z = b[2 * t], w = b[2 * t + 1];
+                a[2 * t] = fmaf(x, c[t], -y * s[t]);
+                a[2 * t + 1] = fmaf(x, s[t], y * c[t]);
+                b[2 * t] = fmaf(z, c[4 + t], -w * s[4 + t]);
+                b[2 * t + 1] = fmaf(z, s[4 + t], w * c[4 + t]);
             }
-            if (p.rotate && r < p.n_q + p.n_kv && lane_on) {
-                if (p.interleaved) {
+        } else {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float2 cs = s_turn[l * 4 + t];
-                        const float a = y[2 * t], b = y[2 * t + 1];
-                        y[2 * t] = fmaf(a, cs.x, -b * cs.y);
-                        y[2 * t + 1] = fmaf(a, cs.y, b * cs.x);
-                    }
-                } else {
-                    const bool low = l < half;
-                    const int i0 = (low ? l : l - half) * 8;
+            for (int t = 0; t < 8; ++t) {
+                const float x = a[t], y = b[t];
+                a[t] = fmaf(x, c[t], -y * s[t]);
+                b[t] = fmaf(x, s[t], y * c[t]);
+            }
+        }
+    };
+
+    // ---- queries
+    const int q1 = min(r1, p.n_q);
+    if (r0 < q1) {
+        const __nv_bfloat16 *src = p.q + (long long)n * p.q_stride;
+        __nv_bfloat16 *dst = p.q_out + (long long)n * p.q_out_stride;
+        for (int base = r0; base < q1; base += RPW * U) {
+            RowHalves x[U];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const float2 cs = s_turn[i0 + t];
-                        const float other = (t & 1) ? bf16_hi(o[t / 2]) : bf16_lo(o[t / 2]);
-                        y[t] = low ? fmaf(y[t], cs.x, -other * cs.y) : fmaf(other, cs.y, y[t] * cs.x);
-                    }
+            for (int u = 0; u < U; ++u) {
+                const int r = base + u * RPW + sub;
+                if (r < q1) x[u] = load(src + r * p.d);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = base + u * RPW + sub;
+                if (r >= q1 || !lane_on) continue;
+                if (p.rotate) {
+                    float a[8], b[8];
+                    unpack8(x[u].lo, a);
+                    unpack8(x[u].hi, b);
+                    turn(a, b);
+                    x[u].lo = pack8(a);
+                    x[u].hi = pack8(b);
                 }
+                *reinterpret_cast<uint4 *>(dst + r * p.d + at) = x[u].lo;
+                *reinterpret_cast<uint4 *>(dst + r * p.d + half + at) = x[u].hi;
             }
-            float a = 0.f;
+        }
+    }
+    // ---- keys, then values
+    if (slot < 0 || slot >= p.n_slots) return;
+    const int page = (int)(slot / p.page_size), prow = (int)(slot - (long long)page * p.page_size);
+    const long long row0 = (long long)page * p.n_kv * p.page_size + prow;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+        const int first = p.n_q + kv * p.n_kv;
+        const int j0 = max(r0 - first, 0), j1 = min(r1 - first, p.n_kv);
+        if (j0 >= j1) continue;
+        const __nv_bfloat16 *src = kv ? p.v_new + (long long)n * p.v_stride : p.k_new + (long long)n * p.k_stride;
+        uint8_t *codes = kv ? p.v_pages : p.k_pages;
+        float *scales = kv ? p.v_scales : p.k_scales;
+        for (int base = j0; base < j1; base += RPW * U) {
+            RowHalves x[U];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) a = fmaxf(a, fabsf(y[t]));     // (fmaxf passes over NaN)
-#pragma unroll
-            for (int m = LPR / 2; m >= 1; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-            if (!row_on || !lane_on) continue;
-            if (r < p.n_q) {
-                uint4 v;
-                v.x = pack_bf16x2(y[0], y[1]);
-                v.y = pack_bf16x2(y[2], y[3]);
-                v.z = pack_bf16x2(y[4], y[5]);
-                v.w = pack_bf16x2(y[6], y[7]);
-                *reinterpret_cast<uint4 *>(p.q_out + (long long)n * p.q_out_stride + (long long)r * p.d + l * 8) = v;
-                continue;
+            for (int u = 0; u < U; ++u) {
+                const int j = base + u * RPW + sub;
+                x[u].lo = x[u].hi = make_uint4(0u, 0u, 0u, 0u);
+                if (j < j1 && lane_on) x[u] = load(src + j * p.d);
             }
-            a = fminf(fmaxf(a, kRowAmaxMin), kRowAmaxMax);
-            const float inv = __fdiv_rn(448.f, a);
-            uint32_t c[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint16_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * t] * inv, y[4 * t + 1] * inv),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                const uint16_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * t + 2] * inv, y[4 * t + 3] * inv),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                c[t] = (uint32_t)lo | ((uint32_t)hi << 16);
+            for (int u = 0; u < U; ++u) {
+                const int j = base + u * RPW + sub;
+                float a[8], b[8];
+                unpack8(x[u].lo, a);
+                unpack8(x[u].hi, b);
+                if (p.rotate && kv == 0 && lane_on) turn(a, b);
+                float m = 0.f;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) m = fmaxf(m, fmaxf(fabsf(a[t]), fabsf(b[t])));     // (passes over NaN)
+#pragma unroll
+                for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (j >= j1 || !lane_on) continue;
+                m = fminf(fmaxf(m, kRowAmaxMin), kRowAmaxMax);
+                const float inv = __fdiv_rn(448.f, m);
+                const long long row = row0 + (long long)j * p.page_size;
+                *reinterpret_cast<uint2 *>(codes + row * p.d + at) = codes8(a, inv);
+                *reinterpret_cast<uint2 *>(codes + row * p.d + half + at) = codes8(b, inv);
+                if (l == 0) scales[row] = __fdiv_rn(m, 448.f);
             }
-            const bool key = r < p.n_q + p.n_kv;
-            const int j = r - p.n_q - (key ? 0 : p.n_kv);
-            const long long row = ((long long)page * p.n_kv + j) * p.page_size + prow;
-            *reinterpret_cast<uint2 *>((key ? p.k_pages : p.v_pages) + row * p.d + l * 8) = make_uint2(c[0], c[1]);
-            if (l == 0) (key ? p.k_scales : p.v_scales)[row] = __fdiv_rn(a, 448.f);
         }
     }
 }
@@ -178,7 +220,7 @@ struct RowGatherParams {
 // Sixteen codes a lane (one 16-byte load, two 16-byte stores); LPR lanes make a row.  A CTA
 // takes consecutive tokens of one head, whose rows lie next to each other within a page.
 // Bound by memory (1 byte read and 2 written per element).
-constexpr int kGatherRows = 2;     // rows a lane has in flight
+constexpr int kGatherRows = 1;     // rows a lane has in flight (with 2 a prompt of 32768 tokens took 41.7 us, with 4 46.2; 39.7)
 template <int LPR>
 __global__ void __launch_bounds__(256) row_gather_kernel(const RowGatherParams p) {
     constexpr int RPC = 256 / LPR;
@@ -206,8 +248,8 @@ __global__ void __launch_bounds__(256) row_gather_kernel(const RowGatherParams p
         code[2 * u] = code[2 * u + 1] = make_uint4(0u, 0u, 0u, 0u);
         sc[2 * u] = sc[2 * u + 1] = 0.f;
         if (row[u] >= 0) {
-            code[2 * u] = __ldg(reinterpret_cast<const uint4 *>(p.k_pages + row[u] * p.d + l * 16));
-            code[2 * u + 1] = __ldg(reinterpret_cast<const uint4 *>(p.v_pages + row[u] * p.d + l * 16));
+            code[2 * u] = __ldcs(reinterpret_cast<const uint4 *>(p.k_pages + row[u] * p.d + l * 16));
+            code[2 * u + 1] = __ldcs(reinterpret_cast<const uint4 *>(p.v_pages + row[u] * p.d + l * 16));
             sc[2 * u] = __ldg(p.k_scales + row[u]);
             sc[2 * u + 1] = __ldg(p.v_scales + row[u]);
         }

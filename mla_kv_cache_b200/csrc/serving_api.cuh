@@ -241,23 +241,26 @@ int kvattn_rope_append_rowscale(const uint16_t *q, const uint16_t *k_new, const 
     p.page_size = page_size;
     p.n_slots = (long long)num_pages * page_size;
     p.rotate = rope_base > 0.f;
-    p.log2_base = p.rotate ? std::log2((double)rope_base) : 0.0;
+    const double log2_base = p.rotate ? std::log2((double)rope_base) : 0.0;
+    for (int i = 0; i < 16; ++i) p.turn_lo[i] = std::exp2(-2.0 * i / head_dim * log2_base) * 0.15915494309189533577;
+    for (int i = 0; i < 8; ++i) p.turn_hi[i] = std::exp2(-2.0 * 16 * i / head_dim * log2_base);
     p.interleaved = interleaved ? 1 : 0;
-    // few tokens: a token's rows are shared out over several CTAs, as many as keep every SM busy
-    const int lpr = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
-    const int at_once = kRowThreads / lpr;
-    const int rows = n_q_heads + 2 * n_kv_heads;
-    int parts = (2 * dev->sms + n_tokens - 1) / n_tokens;
+    // few tokens: a token's rows are shared out over several warps, as many as keep every SM busy
+    const int lpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
+    const int at_once = 32 / lpr, rows = n_q_heads + 2 * n_kv_heads;
+    int parts = (int)((16ll * dev->sms + n_tokens - 1) / n_tokens);
     if (parts > (rows + at_once - 1) / at_once) parts = (rows + at_once - 1) / at_once;
-    p.rows_per_cta = (rows + parts - 1) / parts;
-    const dim3 grid((unsigned)n_tokens, (unsigned)((rows + p.rows_per_cta - 1) / p.rows_per_cta), 1);
+    p.rows_per_part = (rows + parts - 1) / parts;
+    p.parts = (rows + p.rows_per_part - 1) / p.rows_per_part;
+    const long long items = (long long)n_tokens * p.parts;
+    const unsigned grid = (unsigned)((items + kRowThreads / 32 - 1) / (kRowThreads / 32));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (lpr == 8)
+    if (lpr == 4)
+        row_append_kernel<4><<<grid, kRowThreads, 0, s>>>(p);
+    else if (lpr == 8)
         row_append_kernel<8><<<grid, kRowThreads, 0, s>>>(p);
-    else if (lpr == 16)
-        row_append_kernel<16><<<grid, kRowThreads, 0, s>>>(p);
     else
-        row_append_kernel<32><<<grid, kRowThreads, 0, s>>>(p);
+        row_append_kernel<16><<<grid, kRowThreads, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail_cuda(e, "row append launch");
     ++t_launches;
@@ -456,9 +459,11 @@ int kvattn_verify_drafts(const void *target_probs, const void *draft_probs, cons
     const int per16 = 16 / size;
     p.vec = aligned16(target_probs) && aligned16(p.q) && strides[0] % per16 == 0 && strides[1] % per16 == 0 &&
             strides[2] % per16 == 0 && strides[3] % per16 == 0;
-    // CTAs a sequence: enough for two on every SM, each with at least a vector a thread
+    // CTAs a sequence: as many as still run at once, each with at least a vector a thread (64
+    // sequences of 128000: 14.7 us with 8, 17.2 with 2, and 29 with CTAs of twice the size that do
+    // not all fit)
     int C = 1;
-    while (C < kVerifyMaxCluster && (long long)batch * C < 2ll * dev->sms && (long long)C * kVerifyThreads * per16 < vocab) C *= 2;
+    while (C < kVerifyMaxCluster && 2ll * C * batch <= (long long)kVerifyPerSm * dev->sms && (long long)C * kVerifyThreads * per16 < vocab) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
