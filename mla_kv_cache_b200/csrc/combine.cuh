@@ -41,6 +41,7 @@ struct CombineParams {
     int min_tiles;         // the decode kernel's minimum tiles per worker
     int q_len;             // new tokens per sequence (rows of a unit: q_len x g)
     int window;            // sliding window (0: none)
+    int unit_cost;         // tiles a unit with any counts for beside its own
     int start_align;       // windowed ranges start at a multiple of this (0: anywhere)
     int unit_split;        // the decode kernel cuts equal units into parts (unit_part_tiles)
 };
@@ -75,9 +76,10 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
     for (int x = threadIdx.x; x < p.B; x += blockDim.x) {
         const int lx = clamp_len(__ldg(p.seq_lens + x), p.T_max);
         const int t = tiles_of(lx - active_start_on(p.start_align, lx, p.q_len, p.window), p.tile);
-        all += t;
+        const int cost = t > 0 ? t + p.unit_cost : 0;
+        all += cost;
         same &= t == t0;
-        if (x < b) before += t;
+        if (x < b) before += cost;
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
         if (threadIdx.x == 0) p.lse[gh] = -INFINITY;
         return;
     }
-    const long long ustart = (long long)before * p.units_per_seq + (long long)i * n_tiles;
+    const long long ustart = (long long)before * p.units_per_seq + (long long)i * (n_tiles + p.unit_cost);
     long long c_first = ustart / W;
     long long c_last = (ustart + n_tiles - 1) / W;
     bool parts = false;   // the decode kernel's unit parts: workers u k .. u k + ceil(n / Wu) - 1, slot 0

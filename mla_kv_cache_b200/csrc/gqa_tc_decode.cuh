@@ -49,12 +49,6 @@
 //     per 2 KB block, one 16-byte row per token;
 //   - V^T is the V tile read MN-major (128 dimensions = one 128-byte row per token);
 //     the value scale and 1/64 fold into the final 1 / row sum.
-// Row scales (RS, an E4M3 cache with one scale per cached row): the key scale multiplies its
-// token's scores, the value scale its token's weights.  The weights fed to the value
-// product are 2^6 * 2^(s - m) * vs, so the maximum that keeps them in E4M3's range runs over
-// s + log2(vs) instead of s; the row sums take the weights without vs, relative to the same
-// m.  A thread owns one token of a tile, so both scales are one load each per tile, issued a
-// tile ahead (the block-table entry, then the scales: two dependent reads).
 // Each thread keeps its token slot's partial row sums per head; at the end of a piece
 // they are reduced the same way and every thread writes its output dimension of every
 // head (final output, or the worker's partial for the split combine).
@@ -66,19 +60,8 @@
 #include "gqa_decode.cuh"
 #include "schedule.cuh"
 #include "tc05.cuh"
-#include "window.cuh"
 
 namespace kvattn {
-
-// A row-scaled E4M3 cache: k_scale / v_scale of GqaParams are 1, out holds bf16.
-struct GqaRowScaleParams : GqaParams {
-    const float *k_rows, *v_rows;   // [pages, n_kv, page_size]
-    int pages;
-    int start_align;                // windowed ranges start at a tile boundary in a paged cache
-};
-template <bool RS> struct GqaParamsOf { using type = GqaParams; };
-template <> struct GqaParamsOf<true> { using type = GqaRowScaleParams; };
-
 namespace gqatc {
 
 constexpr int TILE = 128;                 // tokens per tile = MMA M
@@ -162,12 +145,6 @@ struct Cfg {
     static constexpr int NTHREADS = 64 + 128 * NG;
 };
 
-// First position of a sequence's tiles.
-__device__ __forceinline__ int first_position(const GqaParams &p, int len) { return active_start(len, p.q_len, p.window); }
-__device__ __forceinline__ int first_position(const GqaRowScaleParams &p, int len) {
-    return active_start_on(p.start_align, len, p.q_len, p.window);
-}
-
 struct Ctx {
     uint8_t *smem;
     Bars *bars;
@@ -246,8 +223,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[NQ]) 
     }
 }
 // ------------------------------------------------------------------ producer (warp 0, lane 0)
-template <int NR, bool KV8, typename P>
-__device__ __forceinline__ void producer(const P &p, const CUtensorMap *kmap, const CUtensorMap *vmap,
+template <int NR, bool KV8>
+__device__ __forceinline__ void producer(const GqaParams &p, const CUtensorMap *kmap, const CUtensorMap *vmap,
                                          const CUtensorMap *qmap, const Ctx &c) {
     using C = Cfg<NR>;
     using L = Kv<KV8>;
@@ -280,7 +257,7 @@ __device__ __forceinline__ void producer(const P &p, const CUtensorMap *kmap, co
             tma_load_4d(qdst, qmap, &bars->qfull[qb], 0, j * p.g, 0, pc.b, pol);
             tma_load_4d(qdst + C::QCHUNK, qmap, &bars->qfull[qb], 64, j * p.g, 0, pc.b, pol);
         }
-        const int start = first_position(p, len);
+        const int start = active_start(len, p.q_len, p.window);
         for (int lt = pc.lt0; lt < pc.lt1; ++lt, ++k) {
             const int s = k % NST;
             const uint32_t ph = (uint32_t)(k / NST) & 1u;
@@ -535,8 +512,8 @@ __device__ __forceinline__ void mma_issuer(const GqaParams &p, const Ctx &c, int
 // (position, head) output rows); without it the kernel keeps the single-token forms --
 // a compile-time split, because the multi-token code in the same kernel costs the
 // single-token MQA workload ~4 us per step (measured) even where it does not run.
-template <int NR, bool KV8, bool MULTI, bool RS>
-__device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::type &p, const Ctx &c, int warp, int lane) {
+template <int NR, bool KV8, bool MULTI>
+__device__ __forceinline__ void softmax_warps(const GqaParams &p, const Ctx &c, int warp, int lane) {
     using C = Cfg<NR, KV8>;
     using L = Kv<KV8>;
     constexpr int NQ = C::NQ;
@@ -580,7 +557,7 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
         const int len = clamp_len(__ldg(p.seq_lens + pc.b), p.T_max);
         const int j = pc.i / p.n_hb, hb = pc.i % p.n_hb;
         const int nt = pc.lt1 - pc.lt0;
-        const int start = first_position(p, len);
+        const int start = active_start(len, p.q_len, p.window);
         // columns of one query position (the group's heads); all columns of the unit
         const uint64_t group_bits = (!MULTI || p.g >= 64) ? ~0ull : ((1ull << p.g) - 1ull);
         // score scale (log2 units); with an E4M3 cache also the key scale and the 2^-e
@@ -596,30 +573,8 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
 #pragma unroll
         for (int h = 0; h < NR; ++h) l_part[h] = 0.f;
 
-        // this thread's token's scales in tile t of the piece (1 where no token is attended to,
-        // and for a page outside the pool, whose codes the TMA unit fills with zeros)
-        auto row_scales = [&](int t) -> float2 {
-            float2 rs = make_float2(1.f, 1.f);
-            if constexpr (RS) {
-                const int tok0 = start + (pc.lt0 + t) * TILE;
-                const int posr = min(tok0, len - TILE) + r;
-                if (t < nt && posr >= tok0 && posr < len) {
-                    const int lp = tok0 / p.page_size;
-                    const int page = p.block_table != nullptr ? __ldg(p.block_table + (size_t)pc.b * p.max_pages + lp) : pc.b;
-                    if (page >= 0 && page < p.pages) {
-                        const size_t row = ((size_t)page * p.n_kv + j) * p.page_size + (posr - lp * p.page_size);
-                        rs = make_float2(__ldg(p.k_rows + row), __ldg(p.v_rows + row));
-                    }
-                }
-            }
-            return rs;
-        };
-        const int t_first = NG == 1 ? 0 : ((g - k) & 1);
-        float2 rs_next = row_scales(t_first);
-        for (int t = t_first; t < nt; t += NG) {
+        for (int t = NG == 1 ? 0 : ((g - k) & 1); t < nt; t += NG) {
             const int kt = k + t;
-            const float2 rs = rs_next;
-            if constexpr (RS) rs_next = row_scales(t + NG);
             const int s = kt % NST, sb = kt & 1;
             const int lt = pc.lt0 + t;
             // tile row r holds position y + r (the last tile is shifted back to end at len;
@@ -667,14 +622,8 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
 #pragma unroll
             for (int h = 0; h < NR; ++h) {
                 const bool see = MULTI ? ((vis >> h) & 1ull) != 0 : in_tile;
-                if constexpr (RS) {
-                    sc[h] = see ? __uint_as_float(sv[h]) * (cs * rs.x) : -INFINITY;
-                    // (the maximum only picks a common factor: a zero scale must not make it -inf)
-                    v[h] = sc[h] + __log2f(fmaxf(rs.y, 8.67361738e-19f));
-                } else {
-                    sc[h] = see ? __uint_as_float(sv[h]) * cs : -INFINITY;
-                    v[h] = sc[h];
-                }
+                sc[h] = see ? __uint_as_float(sv[h]) * cs : -INFINITY;
+                v[h] = sc[h];
             }
             // ---- per-column maximum over the tile's 128 tokens
             warp_xreduce<NR, true>(v, lane);
@@ -740,7 +689,6 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
                                 // 2^6 * 2^(s - m), summed in the same units
                                 a[u] = fast_exp2(sc[h + u] - (mu == -INFINITY ? 0.f : mu) + P8_LOG2);
                                 l_part[h + u] += a[u];
-                                if constexpr (RS) a[u] *= rs.y;
                             }
                             uint16_t h0, l0, h1, l1;
                             split_e4m3x2(a[0], a[1], h0, l0);
@@ -872,13 +820,8 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
             for (int h = 0; h < 16; ++h) {
                 const int cc = c0 + h;
                 if (cc < NR && cc < h_real) {
-                    const float o = (__uint_as_float(ov[h]) + __uint_as_float(ol[h])) * linv[cc];
-                    if (RS && pc.whole) {
-                        reinterpret_cast<__nv_bfloat16 *>(p.out)[out_row(cc) * D + r] = __float2bfloat16_rn(o);
-                    } else {
-                        float *dst = pc.whole ? p.out + out_row(cc) * D : p.ws_o + (part + cc) * D;
-                        dst[r] = o;
-                    }
+                    float *dst = pc.whole ? p.out + out_row(cc) * D : p.ws_o + (part + cc) * D;
+                    dst[r] = (__uint_as_float(ov[h]) + __uint_as_float(ol[h])) * linv[cc];
                 }
             }
         }
@@ -889,9 +832,9 @@ __device__ __forceinline__ void softmax_warps(const typename GqaParamsOf<RS>::ty
 
 }  // namespace gqatc
 
-template <int NR, bool KV8, bool MULTI, bool RS = false>
+template <int NR, bool KV8, bool MULTI>
 __global__ void __launch_bounds__(gqatc::Cfg<NR, KV8>::NTHREADS, 1)
-gqa_tc_decode_kernel(const typename GqaParamsOf<RS>::type p, const __grid_constant__ CUtensorMap kmap,
+gqa_tc_decode_kernel(const GqaParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     using namespace gqatc;
     extern __shared__ uint8_t smem_raw[];
@@ -932,12 +875,7 @@ gqa_tc_decode_kernel(const typename GqaParamsOf<RS>::type p, const __grid_consta
         tmem_alloc(smem_u32(tmem_ptr), Kv<KV8>::TM_COLS);
         tmem_relinquish();
     }
-    if (warp == 2) {
-        if constexpr (RS)
-            build_tile_prefix_on(p.start_align, p.seq_lens, p.B, p.T_max, TILE, s_prefix, lane, p.q_len, p.window);
-        else
-            build_tile_prefix(p.seq_lens, p.B, p.T_max, TILE, s_prefix, lane, p.q_len, p.window);
-    }
+    if (warp == 2) build_tile_prefix(p.seq_lens, p.B, p.T_max, TILE, s_prefix, lane, p.q_len, p.window);
     // query buffers start zeroed: rows a unit's block does not fill stay finite (a
     // single-token block is a full box: the TMA fills its rows past the heads with zeros)
     if constexpr (MULTI)
@@ -993,7 +931,7 @@ gqa_tc_decode_kernel(const typename GqaParamsOf<RS>::type p, const __grid_consta
         } else if (warp == 1) {
             mma_issuer<NR, KV8>(p, c, lane);
         } else {
-            softmax_warps<NR, KV8, MULTI, RS>(p, c, warp, lane);
+            softmax_warps<NR, KV8, MULTI>(p, c, warp, lane);
         }
     }
 

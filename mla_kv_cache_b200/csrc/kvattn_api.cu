@@ -16,6 +16,7 @@
 #include "mla_decode.cuh"
 #include "prefix_decode.cuh"
 #include "rope_append.cuh"
+#include "rs_decode.cuh"
 #include "rowscale.cuh"
 #include "verify.cuh"
 
@@ -481,6 +482,7 @@ int run_gqa(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &v
     cp.min_tiles = p.min_tiles;
     cp.q_len = 1;
     cp.window = 0;
+    cp.unit_cost = 0;
     cp.start_align = 0;
     cp.unit_split = 0;
     const int rows = p.g < C::HEADS ? p.g : C::HEADS;
@@ -490,10 +492,10 @@ int run_gqa(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &v
 
 // The tcgen05 kernel (gqa_tc_decode.cuh): tokens on the MMA rows, up to 64 query heads
 // per unit, NR head columns processed.
-template <int NR, bool KV8, bool RS = false>
-int run_gqa_tc(const typename GqaParamsOf<RS>::type &base, const CUtensorMap &kmap, const CUtensorMap &vmap,
+template <int NR, bool KV8>
+int run_gqa_tc(const GqaParams &base, const CUtensorMap &kmap, const CUtensorMap &vmap,
                const CUtensorMap &qmap, DeviceState *dev, int units_per_seq, cudaStream_t stream) {
-    typename GqaParamsOf<RS>::type p = base;
+    GqaParams p = base;
     p.unit_split = 1;   // equal units are cut into parts of one unit each (schedule.cuh)
     const int smem = gqatc::smem_bytes(p.B);
     if (smem > dev->max_smem_optin) {
@@ -525,8 +527,7 @@ int run_gqa_tc(const typename GqaParamsOf<RS>::type &base, const CUtensorMap &km
     p.ws_o = reinterpret_cast<float *>(static_cast<char *>(ws) + meta_bytes + lse_bytes);
 
     // several new tokens or a window: the instantiation with the visibility mask
-    auto kern = (p.q_len > 1 || p.window > 0) ? gqa_tc_decode_kernel<NR, KV8, true, RS>
-                                              : gqa_tc_decode_kernel<NR, KV8, false, RS>;
+    auto kern = (p.q_len > 1 || p.window > 0) ? gqa_tc_decode_kernel<NR, KV8, true> : gqa_tc_decode_kernel<NR, KV8, false>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), dev, smem);
     if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(gqa tc)");
     kern<<<p.workers, gqatc::Cfg<NR, KV8>::NTHREADS, smem, stream>>>(p, kmap, vmap, qmap);
@@ -553,12 +554,74 @@ int run_gqa_tc(const typename GqaParamsOf<RS>::type &base, const CUtensorMap &km
     cp.min_tiles = p.min_tiles;
     cp.q_len = p.q_len;
     cp.window = p.window;
+    cp.unit_cost = 0;
     cp.start_align = 0;
-    if constexpr (RS) cp.start_align = p.start_align;
     cp.unit_split = p.unit_split;
     const int rows = p.g * p.q_len < gqatc::HB ? p.g * p.q_len : gqatc::HB;
     return launch_combine(gqatc::D, cp, p.B * units_per_seq, rows, stream,
-                          combine_warps((p.T_max + gqatc::TILE - 1) / gqatc::TILE, max_tiles, p.workers), RS);
+                          combine_warps((p.T_max + gqatc::TILE - 1) / gqatc::TILE, max_tiles, p.workers));
+}
+
+// The row-scaled E4M3 kernel (rs_decode.cuh): MT m-tiles of 16 query rows, NR of each in use.
+template <int MT, int NR>
+int run_rs(const RsParams &base, const CUtensorMap &kmap, const CUtensorMap &vmap, DeviceState *dev, cudaStream_t stream) {
+    RsParams p = base;
+    constexpr int ROWS = 16 * MT;
+    const int smem = rs::smem_bytes(p.B);
+    if (smem > dev->max_smem_optin) {
+        snprintf(t_detail, sizeof(t_detail), "needs %d B shared memory", smem);
+        return KVATTN_ERR_UNSUPPORTED;
+    }
+    const int unit_tiles = (p.T_max + rs::TILE - 1) / rs::TILE;
+    const long long max_tiles = (long long)p.B * p.n_kv * unit_tiles;
+    p.min_tiles = g_force_min_tiles > 0 ? g_force_min_tiles : (unit_tiles < 2 ? 1 : 2);
+    long long workers = g_force_workers > 0 ? g_force_workers : dev->sms;
+    const long long by_size = (max_tiles + p.min_tiles - 1) / p.min_tiles;
+    if (g_force_workers <= 0 && workers > by_size) workers = by_size;
+    p.workers = (int)workers;
+
+    void *ws = nullptr;
+    const size_t lse_bytes = (((size_t)p.workers * 2 * ROWS * 4) + 255) & ~size_t(255);
+    const size_t o_bytes = (size_t)p.workers * 2 * ROWS * rs::D * 4;
+    {
+        std::lock_guard<std::mutex> lk(g_mutex);
+        int st = ensure_workspace(dev, lse_bytes + o_bytes, &ws);
+        if (st != KVATTN_OK) return st;
+    }
+    p.ws_lse = reinterpret_cast<float *>(ws);
+    p.ws_o = reinterpret_cast<float *>(static_cast<char *>(ws) + lse_bytes);
+    auto kern = rs_decode_kernel<MT, NR>;
+    cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), dev, smem);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(row-scaled decode)");
+    kern<<<p.workers, rs::NTHREADS, smem, stream>>>(p, kmap, vmap);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail_cuda(e, "row-scaled decode launch");
+    ++t_launches;
+
+    CombineParams cp = {};
+    cp.seq_lens = p.seq_lens;
+    cp.ws_lse = p.ws_lse;
+    cp.ws_o = p.ws_o;
+    cp.out = p.out;
+    cp.lse = p.lse;
+    cp.B = p.B;
+    cp.n_q = p.n_q;
+    cp.units_per_seq = p.n_kv;
+    cp.heads_per_unit = ROWS;
+    cp.n_hb = 1;
+    cp.n_kv = p.n_kv;
+    cp.g = p.g;
+    cp.T_max = p.T_max;
+    cp.tile = rs::TILE;
+    cp.workers = p.workers;
+    cp.min_tiles = p.min_tiles;
+    cp.q_len = p.q_len;
+    cp.window = p.window;
+    cp.unit_cost = rs::unit_cost(MT);
+    cp.start_align = p.start_align;
+    cp.unit_split = 1;
+    return launch_combine(rs::D, cp, p.B * p.n_kv, p.g * p.q_len, stream,
+                          combine_warps(unit_tiles, max_tiles, p.workers), true);
 }
 
 // Which GQA kernel runs: the tcgen05 kernel for head_dim 128 once a group has a few
@@ -583,7 +646,6 @@ struct GqaCache {
     bool e4m3 = false;            // E4M3 codes (value = code * scale) instead of bf16
     float k_scale = 1.f, v_scale = 1.f;
     bool one_page = false;        // every sequence's rows lie in its first page
-    const float *k_rows = nullptr, *v_rows = nullptr;   // a scale per cached row (E4M3; out is then bf16)
 };
 
 // ---------------------------------------------------------------------------------------
@@ -759,18 +821,6 @@ int gqa_decode_impl(const uint16_t *q, const GqaCache &cache, const int32_t *seq
     p.v_scale = cache.v_scale;
     const int U = n_kv_heads * n_hb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tc && cache.k_rows) {
-        GqaRowScaleParams rp = {};
-        static_cast<GqaParams &>(rp) = p;
-        rp.k_rows = cache.k_rows;
-        rp.v_rows = cache.v_rows;
-        rp.pages = (int)cache.pages;
-        rp.start_align = cache.block_table && !cache.one_page ? gqatc::TILE : 0;
-        if (gl > 32) return run_gqa_tc<64, true, true>(rp, kmap, vmap, qmap, dev, U, s);
-        if (gl > 16) return run_gqa_tc<32, true, true>(rp, kmap, vmap, qmap, dev, U, s);
-        if (gl > 8) return run_gqa_tc<16, true, true>(rp, kmap, vmap, qmap, dev, U, s);
-        return run_gqa_tc<8, true, true>(rp, kmap, vmap, qmap, dev, U, s);
-    }
     if (tc && cache.e4m3) {
         if (gl > 32) return run_gqa_tc<64, true>(p, kmap, vmap, qmap, dev, U, s);
         if (gl > 16) return run_gqa_tc<32, true>(p, kmap, vmap, qmap, dev, U, s);
@@ -788,6 +838,62 @@ int gqa_decode_impl(const uint16_t *q, const GqaCache &cache, const int32_t *seq
                        : run_gqa<128, 2>(p, kmap, vmap, dev, U, s, noalloc);
     return MT == 1 ? run_gqa<64, 1>(p, kmap, vmap, dev, U, s, noalloc)
                    : run_gqa<64, 2>(p, kmap, vmap, dev, U, s, noalloc);
+}
+
+// Decode over a row-scaled E4M3 cache.  New tokens whose (position, head) rows exceed the
+// kernel's 64 run as a virtual batch of single-token sequences.
+int rs_decode_impl(const uint16_t *q, const GqaCache &cache, const float *k_rows, const float *v_rows,
+                   const int32_t *seq_lens, int batch, int n_q_heads, int n_kv_heads, float scale, void *out, float *lse,
+                   cudaStream_t stream, int q_len, int window) {
+    DeviceState *dev = nullptr;
+    int st = device_state(&dev);
+    if (st != KVATTN_OK) return st;
+    const int g = n_q_heads / n_kv_heads, rows = g * q_len;
+    if (rows > 64 && q_len > 1) {
+        int32_t *vlens = nullptr, *vtable = nullptr;
+        st = virtual_batch(dev, seq_lens, cache.block_table, batch, q_len, cache.max_pages, cache.capacity, stream, &vlens,
+                           &vtable);
+        if (st != KVATTN_OK) return st;
+        GqaCache vc = cache;
+        vc.block_table = vtable;
+        vc.max_pages = cache.block_table ? cache.max_pages : 1;
+        vc.one_page = cache.block_table == nullptr;
+        return rs_decode_impl(q, vc, k_rows, v_rows, vlens, batch * q_len, n_q_heads, n_kv_heads, scale, out, lse, stream, 1,
+                              window);
+    }
+    CUtensorMap maps[2];
+    const void *base[2] = {cache.k, cache.v};
+    for (int i = 0; i < 2; ++i) {
+        // (a row of 128 codes as 64 two-byte elements: the TMA moves bytes)
+        st = encode_map_3d(&maps[i], base[i], rs::D / 2, cache.page_size, (uint64_t)cache.pages * n_kv_heads, 64, rs::TILE,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != KVATTN_OK) return st;
+    }
+    RsParams p = {};
+    p.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p.seq_lens = seq_lens;
+    p.out = static_cast<float *>(out);
+    p.lse = lse;
+    p.B = batch;
+    p.n_q = n_q_heads;
+    p.n_kv = n_kv_heads;
+    p.T_max = cache.capacity;
+    p.g = g;
+    p.n_hb = 1;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.block_table = cache.block_table;
+    p.max_pages = cache.max_pages;
+    p.page_size = cache.page_size;
+    p.q_len = q_len;
+    p.window = window;
+    p.k_rows = k_rows;
+    p.v_rows = v_rows;
+    p.pages = (int)cache.pages;
+    p.start_align = cache.block_table && !cache.one_page ? rs::TILE : 0;
+    if (rows > 32) return run_rs<4, 16>(p, maps[0], maps[1], dev, stream);
+    if (rows > 16) return run_rs<2, 16>(p, maps[0], maps[1], dev, stream);
+    if (rows > 8) return run_rs<1, 16>(p, maps[0], maps[1], dev, stream);
+    return run_rs<1, 8>(p, maps[0], maps[1], dev, stream);
 }
 
 // A latent + rotary-key cache as the MLA kernel sees it (pages of page_size rows; a

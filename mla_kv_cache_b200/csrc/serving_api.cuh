@@ -335,7 +335,7 @@ int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const 
     if (n_q_heads % n_kv_heads != 0) return KVATTN_ERR_INVALID_ARG;
     if (!block_table && (num_pages != batch || max_pages_per_seq != 1)) return KVATTN_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return KVATTN_ERR_INVALID_ARG;
-    if (head_dim != 128 || n_q_heads / n_kv_heads > gqatc::HB || (block_table && page_size % gqatc::TILE != 0))
+    if (head_dim != 128 || n_q_heads / n_kv_heads > 64 || (block_table && page_size % rs::TILE != 0))
         return KVATTN_ERR_UNSUPPORTED;
     if ((long long)batch * q_len > kMaxBatch || (long long)max_pages_per_seq * page_size >= (1ll << 31))
         return KVATTN_ERR_UNSUPPORTED;
@@ -351,11 +351,8 @@ int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const 
             return KVATTN_ERR_INVALID_ARG;
     if (overlaps(out, rows * head_dim * 2, lse, rows * 4)) return KVATTN_ERR_INVALID_ARG;
     GqaCache cache{k_pages, v_pages, block_table, max_pages_per_seq * page_size, page_size, max_pages_per_seq, num_pages};
-    cache.e4m3 = true;
-    cache.k_rows = k_scales;
-    cache.v_rows = v_scales;
-    return gqa_decode_impl(q, cache, seq_lens, batch, n_q_heads, n_kv_heads, head_dim, scale,
-                           reinterpret_cast<float *>(out), lse, stream, q_len, window);
+    return rs_decode_impl(q, cache, k_scales, v_scales, seq_lens, batch, n_q_heads, n_kv_heads, scale, out, lse,
+                          static_cast<cudaStream_t>(stream), q_len, window);
 }
 
 int kvattn_gqa_decode_prefix_workspace(int max_prefix_len, int max_seq_len, int batch, int q_len, int n_q_heads,

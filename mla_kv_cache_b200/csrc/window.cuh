@@ -14,8 +14,9 @@ __device__ __forceinline__ int active_start_on(int align, int len, int q_len, in
     return align > 1 ? s - s % align : s;
 }
 
-// build_tile_prefix (schedule.cuh) over those ranges.
-__device__ __forceinline__ void build_tile_prefix_on(int align, const int32_t *seq_lens, int B, int T_max, int tile,
+// build_tile_prefix (schedule.cuh) over those ranges; a sequence with tiles counts `cost` more, what a
+// unit's start and end cost in tiles.
+__device__ __forceinline__ void build_tile_prefix_on(int align, int cost, const int32_t *seq_lens, int B, int T_max, int tile,
                                                      int *s_prefix, int lane, int q_len, int window) {
     int running = 0;
     if (lane == 0) s_prefix[0] = 0;
@@ -25,6 +26,7 @@ __device__ __forceinline__ void build_tile_prefix_on(int align, const int32_t *s
         if (idx < B) {
             const int len = clamp_len(__ldg(seq_lens + idx), T_max);
             v = tiles_of(len - active_start_on(align, len, q_len, window), tile);
+            if (v > 0) v += cost;
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
