@@ -97,10 +97,8 @@ constexpr int CHUNK = 128 * 128;          // [128 rows x 128 bytes]
 constexpr int NS_MAX = 10;
 constexpr float RESCALE = 8.f, LIMIT = 64.f;
 // Line positions (see above), and the least a worker takes.
-constexpr uint32_t WP2 = 4, WP1 = 2, WS = 4, W_MIN = 4;
+constexpr uint32_t WP2 = 8, WP1 = 6, WS = 6, US = 3, W_MIN = 8;
 constexpr long long LINE_LIMIT = 1ll << 30;
-// Of every eight pairs of exponentials, this many are taken on the FMA pipe.
-constexpr int POLY = 0;
 
 // Two fp32 values in one 64-bit register pair: one instruction works on both.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -125,29 +123,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-
-// 2^x of a pair on the FMA pipe (x <= 100; below -126 it is 2^-126, nothing next to a sum of weights):
-// x = n + r with n the nearest integer (adding 1.5 * 2^23 leaves n in the low mantissa bits),
-// 2^r for |r| <= 1/2 by a polynomial of degree 4 -- fitted to the least maximal relative error,
-// 2.6e-6, a hundredth of the weight's bf16 step -- and n added to its exponent field.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-    float a, b;
-    unpack2(x2, a, b);
-    x2 = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
-    const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
-    const uint64_t t = add2(x2, magic);
-    const uint64_t r = fma2(add2(t, unmagic), pack2(-1.f, -1.f), x2);
-    uint64_t y = pack2(0.00957010160f, 0.00957010160f);
-    y = fma2(y, r, pack2(0.0559178621f, 0.0559178621f));
-    y = fma2(y, r, pack2(0.240247448f, 0.240247448f));
-    y = fma2(y, r, pack2(0.693121815f, 0.693121815f));
-    y = fma2(y, r, pack2(0.999999261f, 0.999999261f));
-    float ta, tb, ya, yb;
-    unpack2(t, ta, tb);
-    unpack2(y, ya, yb);
-    return pack2(__uint_as_float(__float_as_uint(ya) + (__float_as_uint(ta) << 23)),
-                 __uint_as_float(__float_as_uint(yb) + (__float_as_uint(tb) << 23)));
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
@@ -214,7 +189,7 @@ static_assert(sizeof(Bars) <= 384, "barrier block overflows its slot");
 
 // ------------------------------------------------------------------ the line of work
 // The suffix table: word b holds, in its upper 25 bits, the sum over the sequences before b of
-// their line units c = tiles + 1 (0 without tokens), and in its lower 7 the last tile's tokens
+// their line units c = tiles + US (0 without tokens), and in its lower 7 the last tile's tokens
 // less one: a sequence's tiles and length without another load.
 __device__ __forceinline__ uint32_t table_units(uint32_t w) { return w >> 7; }
 
@@ -231,9 +206,10 @@ __device__ __forceinline__ void build_table(const int32_t *seq_lens, int B, int 
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (base + 32 * u >= B) break;
             const int i = base + 32 * u + lane;
             const uint32_t nt = (uint32_t)tiles_of(len[u], TILE);
-            const uint32_t c = nt ? nt + 1 : 0;
+            const uint32_t c = nt ? nt + US : 0;
             uint32_t s = c;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -360,7 +336,7 @@ __device__ __forceinline__ bool walk_next(Walk &k, const PrefixParams &p, const 
                 c.b = lo;
                 const uint32_t w0 = tab[lo];
                 const uint32_t cu = table_units(tab[lo + 1]) - table_units(w0);
-                c.len = (int)((cu - 2) * TILE + (w0 & 127u) + 1);
+                c.len = (int)((cu - US - 1) * TILE + (w0 & 127u) + 1);
                 c.j = (int)((k.pos - l.p_total - table_units(w0) * (uint32_t)p.n_kv * WS) / (cu * WS));
                 c.prefix = false;
                 k.u0 = l.p_total + (table_units(w0) * (uint32_t)p.n_kv + (uint32_t)c.j * cu) * WS;
@@ -571,22 +547,15 @@ __device__ __forceinline__ float weights64(const float *s, float cs, float m, ui
     for (int e = 0; e < 32; ++e) {
         const uint64_t z = fma2(pack2(s[2 * e], s[2 * e + 1]), cs2, off2);
         float a, b;
-        if (e % 8 < POLY) {
-            const uint64_t v = exp2_poly2(z);
-            l2[e & 1] = add2(l2[e & 1], v);
-            unpack2(v, a, b);
-        } else {
-            unpack2(z, a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            l2[e & 1] = add2(l2[e & 1], pack2(a, b));
-        }
+        unpack2(z, a, b);
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        l2[e & 1] = add2(l2[e & 1], pack2(a, b));
         w[e] = pack_bf16x2(a, b);
     }
     float la, lb;
     unpack2(add2(l2[0], l2[1]), la, lb);
-    // (a row that has seen nothing yet has no sum: the polynomial's weights do not reach zero)
-    return m == -INFINITY ? 0.f : la + lb;
+    return la + lb;
 }
 __device__ __forceinline__ float max128(const float *s) {
     float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
@@ -870,7 +839,7 @@ __global__ void __launch_bounds__(32) prefix_table_kernel(const PrefixParams p) 
 // (the table, the partials, the stores), not its bytes: the partials' addresses follow from the
 // table alone, so the log-sum-exps and the values of up to MC_P prefix and MC_S suffix partials are
 // loaded together, without branches (places that hold no partial are read and dropped).  8 sequences
-// behind 2000 tokens: 23.4 us a call with loads that wait for the log-sum-exps, @@ so.
+// behind 2000 tokens: 23.4 us a call with loads that wait for the log-sum-exps, 19.3 us so.
 // The result goes through shared memory to be written in whole rows.
 constexpr int kMergeWarps = 8;
 namespace pfx {
@@ -961,7 +930,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
 #pragma unroll
         for (int k = 0; k < MC_S; ++k) {
             uint32_t a, z;
-            suffix_piece(l, sa, cu - 1, (uint32_t)(v0 + ((i0 + k) >> 1)), a, z);
+            suffix_piece(l, sa, cu - US, (uint32_t)(v0 + ((i0 + k) >> 1)), a, z);
             if (i0 + k >= ns || a >= z) x[k] = -INFINITY;
         }
     };
