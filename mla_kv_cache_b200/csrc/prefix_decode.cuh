@@ -91,7 +91,7 @@ constexpr int ROWS = 128;
 constexpr int NTHREADS = 384;
 // registers of a thread after the split between the first warpgroup (producer, issuers) and the
 // softmax warpgroups: a row's 128 scores and its packed weights stay in registers
-constexpr int REGS_LAUNCH = 168, REGS_CTRL = 80, REGS_SOFT = 208;
+constexpr int REGS_LAUNCH = 168, REGS_CTRL = 56, REGS_SOFT = 224;
 static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= NTHREADS * REGS_LAUNCH, "registers of the launch");
 constexpr int CHUNK = 128 * 128;          // [128 rows x 128 bytes]
 constexpr int NS_MAX = 10;
@@ -170,16 +170,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         : "memory");
 }
 
-// tensor memory columns of group x: scores (and weights) at 128 x, output at 256 + 128 x
-constexpr uint32_t TM_S = 0, TM_O = 256, TM_X = 128;
+// Tensor memory columns: NSB score buffers of 128, the groups' weights (bf16 pairs, 64 columns
+// each), the groups' outputs (D columns each); all 512 for either head size.
+template <int D>
+struct Tm {
+    static constexpr uint32_t NSB = D == 64 ? 2 : 1;
+    static constexpr uint32_t S = 0, P = 128 * NSB, O = 512 - 2 * D;
+    static_assert(P + 2 * 64 == O, "columns");
+};
 
 struct Bars {
     uint64_t full[NS_MAX], empty[NS_MAX];
     uint64_t qfull[2], qempty[2];
-    uint64_t sready[2];      // group x's next scores are in TMEM (and its value product before is done)
+    uint64_t sready[2];      // group x's next scores are in tensor memory
+    uint64_t sfree[2];       // [buffer] the scores have been read
     uint64_t pready[2][2];   // [group][half] the weights are written (and O_x rescaled)
-    uint64_t turn[2];        // group x may issue its next products
-    uint64_t odone[2];       // group x's last value product of a piece is done
+    uint64_t pdone[2];       // group x's value product is done
     uint64_t ofree[2];       // group x has read O_x
     uint32_t tmem;
     int prefix_len;
@@ -431,109 +437,80 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
 }
 
 // ------------------------------------------------------------------ MMA issuers (warps 1 and 2, lane 0)
-// Value product n of the group in two halves, then its score product n + 1: the latter overwrites
-// the weights that the former reads, and one thread's MMAs run in order.  The two issuers take
-// turns with the second half and the scores, in the order of the steps, so that one group's
-// products are queued together (a group whose next tiles have not landed gives its turn away
-// before the scores).
+// Step n of the CTA belongs to group n & 1.  The tiles are given back by the commits behind their
+// last products.
+// S = Q K^T of every step, into the score buffers in turn.
 template <int D>
-__device__ __forceinline__ void mma_issuer(const PrefixParams &p, const Ctx &c, int x) {
+__device__ __forceinline__ void score_issuer(const PrefixParams &p, const Ctx &c) {
+    using C = Cfg<D>;
+    constexpr uint32_t NSB = Tm<D>::NSB;
+    Bars *bars = c.bars;
+    const uint32_t smem = smem_u32(c.smem);
+    constexpr uint32_t idesc = idesc_f16_major(128, TILE, 1, 1, 0, 0);
+    const int qoff_suffix = suffix_shift(p.L * p.g) * 128;
+    uint32_t n = 0;
+    Walk k = walk_start(c.line, c.w);
+    while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
+        const Piece &pc = k.pc;
+        for (int i = 0; i < pc.steps; ++i, ++n) {
+            const uint32_t x = n & 1u, buf = n % NSB;
+            const int qslot = pc.two ? (k.qs + i) & 1 : k.qs;
+            const uint32_t nk = 2 * (k.tiles + (uint32_t)(pc.two ? i >> 1 : i)), slot = nk % C::NS;
+            if (i < (pc.two ? 2 : 1) &&
+                !mbar_wait(&bars->qfull[qslot], ((qslot ? k.quse1 : k.quse0) - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag))
+                return;
+            if (!mbar_wait(&bars->full[slot], (nk / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+            if (n >= NSB && !mbar_wait(&bars->sfree[buf], (n / NSB - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
+            tc_fence_after();
+            const uint32_t ts = bars->tmem + Tm<D>::S + 128 * buf;
+            const uint32_t q = desc_lo(smem + C::OFF_Q + qslot * C::Q_BYTES - (!pc.prefix && x == 1 ? qoff_suffix : 0), 16);
+            const uint32_t kt = desc_lo(smem + slot * C::KV_BYTES, 16);
+            mma_ss<false>(ts, q, kt, idesc);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * CHUNK + (kk & 3) * 32) >> 4;
+                mma_ss<true>(ts, q + off, kt + off, idesc);
+            }
+            umma_commit(&bars->sready[x]);
+            if (!pc.two || (i & 1)) umma_commit(&bars->empty[slot]);
+            if (i + (pc.two ? 2 : 1) >= pc.steps) umma_commit(&bars->qempty[qslot]);
+        }
+    }
+}
+// O_x += P_x V of every step, each in two halves of 64 tokens as the weights come.
+template <int D>
+__device__ __forceinline__ void value_issuer(const PrefixParams &p, const Ctx &c) {
     using C = Cfg<D>;
     Bars *bars = c.bars;
     const uint32_t smem = smem_u32(c.smem);
-    const uint32_t ts = bars->tmem + TM_S + TM_X * x, to = bars->tmem + TM_O + TM_X * x;
-    constexpr uint32_t idesc_qk = idesc_f16_major(128, TILE, 1, 1, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_f16_major(128, D, 1, 1, 0, 1);
+    constexpr uint32_t idesc = idesc_f16_major(128, D, 1, 1, 0, 1);
+    uint32_t n = 0, pieces[2] = {0, 0};
     Walk k = walk_start(c.line, c.w);
-    int i = 0, i0 = 0;                     // the step and the group's first step of the piece
-    auto next_piece = [&]() -> bool {      // to the next piece in which this group has a step
-        while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
-            i = i0 = (int)((k.steps & 1u) ^ (uint32_t)x);
-            if (i < k.pc.steps) return true;
-        }
-        return false;
-    };
-    struct Step {
-        uint32_t nk, kslot, vslot, qpar;
-        int qslot, qoff;
-        bool first, last;
-    };
-    const int qoff_suffix = x == 1 ? suffix_shift(p.L * p.g) * 128 : 0;
-    auto step = [&]() -> Step {
-        Step s;
-        s.nk = 2 * (k.tiles + (uint32_t)(k.pc.two ? i >> 1 : i));
-        s.kslot = s.nk % C::NS;
-        s.vslot = (s.nk + 1) % C::NS;
-        s.qslot = k.pc.two ? (k.qs + i0) & 1 : k.qs;
-        s.qpar = ((s.qslot ? k.quse1 : k.quse0) - 1) & 1u;
-        s.qoff = k.pc.prefix ? 0 : qoff_suffix;
-        s.first = i == i0;
-        s.last = i + 2 >= k.pc.steps;
-        return s;
-    };
-    auto landed = [&](const Step &s) -> bool {
-        return (!s.first || mbar_test(&bars->qfull[s.qslot], s.qpar)) &&
-               mbar_test(&bars->full[s.kslot], (s.nk / C::NS) & 1u);
-    };
-    auto wait_landed = [&](const Step &s) -> bool {
-        if (s.first && !mbar_wait(&bars->qfull[s.qslot], s.qpar, FLAG_FULL_WAIT, c.abort_flag)) return false;
-        return mbar_wait(&bars->full[s.kslot], (s.nk / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag);
-    };
-    auto scores = [&](const Step &s) {
-        const uint32_t q = desc_lo(smem + C::OFF_Q + s.qslot * C::Q_BYTES - s.qoff, 16);
-        const uint32_t kt = desc_lo(smem + s.kslot * C::KV_BYTES, 16);
-        mma_ss<false>(ts, q, kt, idesc_qk);
-#pragma unroll
-        for (int kk = 1; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * CHUNK + (kk & 3) * 32) >> 4;
-            mma_ss<true>(ts, q + off, kt + off, idesc_qk);
-        }
-        umma_commit(&bars->sready[x]);
-    };
-    if (!next_piece()) return;
-    Step cur = step();
-    if (!wait_landed(cur)) return;
-    tc_fence_after();
-    scores(cur);
-    uint32_t pieces = 0;                   // pieces whose last value product is issued
-    for (uint32_t n = 0;; ++n) {
-        bool more = true;
-        i += 2;
-        if (cur.last) more = next_piece();
-        Step nxt = cur;
-        if (more) nxt = step();
-        if (!mbar_wait(&bars->full[cur.vslot], ((cur.nk + 1) / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-        if (cur.first && pieces > 0 && !mbar_wait(&bars->ofree[x], (pieces - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-        if (!mbar_wait(&bars->pready[x][0], n & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-        tc_fence_after();
-        const uint32_t vt = desc_lo(smem + cur.vslot * C::KV_BYTES, CHUNK);
-        if (cur.first) mma_ts<false>(to, ts, vt, idesc_pv);
-        else mma_ts<true>(to, ts, vt, idesc_pv);
-#pragma unroll
-        for (int kk = 1; kk < TILE / 32; ++kk) mma_ts<true>(to, ts + kk * 8, vt + kk * (2048 >> 4), idesc_pv);
-        if (!mbar_wait(&bars->pready[x][1], n & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-        const uint32_t turn = n - (x == 0 ? 1u : 0u);
-        if (turn != ~0u && !mbar_wait(&bars->turn[x], turn & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = TILE / 32; kk < TILE / 16; ++kk) mma_ts<true>(to, ts + kk * 8, vt + kk * (2048 >> 4), idesc_pv);
-        if (cur.last) {
-            umma_commit(&bars->odone[x]);
-            ++pieces;
-        }
-        const bool now = more && landed(nxt);
-        if (now) {
+    while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
+        const Piece &pc = k.pc;
+        for (int i = 0; i < pc.steps; ++i, ++n) {
+            const uint32_t x = n & 1u, par = (n >> 1) & 1u;
+            const uint32_t nv = 2 * (k.tiles + (uint32_t)(pc.two ? i >> 1 : i)) + 1, slot = nv % C::NS;
+            if (!mbar_wait(&bars->full[slot], (nv / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+            if (i < 2) {
+                const uint32_t before = x ? pieces[1]++ : pieces[0]++;
+                if (before > 0 && !mbar_wait(&bars->ofree[x], (before - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
+            }
+            const uint32_t tp = bars->tmem + Tm<D>::P + 64 * x, to = bars->tmem + Tm<D>::O + D * x;
+            const uint32_t vt = desc_lo(smem + slot * C::KV_BYTES, CHUNK);
+            if (!mbar_wait(&bars->pready[x][0], par, FLAG_MMA_WAIT, c.abort_flag)) return;
             tc_fence_after();
-            scores(nxt);
-        }
-        mbar_arrive(&bars->turn[x ^ 1]);
-        if (!more) return;
-        if (!now) {
-            if (!wait_landed(nxt)) return;
+            if (i < 2) mma_ts<false>(to, tp, vt, idesc);
+            else mma_ts<true>(to, tp, vt, idesc);
+#pragma unroll
+            for (int kk = 1; kk < TILE / 32; ++kk) mma_ts<true>(to, tp + kk * 8, vt + kk * (2048 >> 4), idesc);
+            if (!mbar_wait(&bars->pready[x][1], par, FLAG_MMA_WAIT, c.abort_flag)) return;
             tc_fence_after();
-            scores(nxt);
+#pragma unroll
+            for (int kk = TILE / 32; kk < TILE / 16; ++kk) mma_ts<true>(to, tp + kk * 8, vt + kk * (2048 >> 4), idesc);
+            if (!pc.two || (i & 1)) umma_commit(&bars->empty[slot]);
+            umma_commit(&bars->pdone[x]);
         }
-        cur = nxt;
     }
 }
 
@@ -594,16 +571,16 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
     const int quad = warp & 3;
     const int lrow = 32 * quad + lane;                // TMEM lane
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const uint32_t ts = tmem + lanes + TM_S + TM_X * x, to = tmem + lanes + TM_O + TM_X * x;
+    constexpr uint32_t NSB = Tm<D>::NSB;
+    const uint32_t tp = tmem + lanes + Tm<D>::P + 64 * x, to = tmem + lanes + Tm<D>::O + D * x;
     const bool negate = p.scale_log2 < 0.f;           // (the maximum is taken of the unscaled scores)
     const float cs = fmaxf(fabsf(p.scale_log2), 1e-30f);   // (a zero scale: masked scores stay -inf)
-    uint32_t n_x = 0, pieces = 0;                     // steps and pieces of this group
+    uint32_t n_x = 0;                                 // steps of this group
     Walk k = walk_start(c.line, c.w);
     const Piece &pc = k.pc;
     while (walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
         const int first = (int)((k.steps & 1u) ^ (uint32_t)x);      // this group's first step of the piece
         const int part = first;                       // row tile (two) or share of the K/V tiles
-        const uint32_t use = pc.two ? 1u : 2u;        // arrivals that free a tile: one of each group, or both from one
         // rows of the tile that are real
         int rows = p.L * p.g;
         if (pc.prefix) {
@@ -617,7 +594,6 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
         // the suffixes come last and all have as many rows: warps without any are done, and the
         // first answers for them
         if (!pc.prefix && !warp_on) return;
-        const bool releases = lane == 0 && q_on == 0;
         const uint32_t arrivals = pc.prefix || q_on > 0 ? 1u : 4u - (uint32_t)((rows - 1) / 32);
         // positions this row sees: all of the prefix; a suffix up to its own token
         const int limit = pc.prefix ? pc.len : pc.len - p.L + 1 + min(r / p.g, p.L - 1);
@@ -626,32 +602,36 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
         for (int i = first; i < pc.steps; i += 2, ++n_x) {
             const int it = pc.two ? i >> 1 : i;
             if (!warp_all(mbar_wait(&bars->sready[x], n_x & 1u, FLAG_MMA_WAIT, c.abort_flag))) return;
-            // the scores are there: this group is done with the K tile, with the V tile of its step
-            // before, and after its last step with Q
-            if (releases) {
-                const uint32_t nk = 2 * (k.tiles + (uint32_t)it);
-                mbar_arrive_n(&bars->empty[nk % C::NS], use);
-                if (i != first) {
-                    const uint32_t nv = nk + 1 - (pc.two ? 2u : 4u);
-                    mbar_arrive_n(&bars->empty[nv % C::NS], use);
-                }
-                if (i + 2 >= pc.steps)
-                    mbar_arrive_n(&bars->qempty[pc.two ? (k.qs + first) & 1 : k.qs], pc.two || pc.steps == 1 ? 2u : 1u);
-            }
+            const uint32_t buf = (2 * n_x + (uint32_t)x) % NSB, ts = tmem + lanes + Tm<D>::S + 128 * buf;
+            // the step before must be through its value product before its weights are overwritten
+            // or O_x is rescaled
+            bool settled = i == first;
+            auto settle = [&]() -> bool {
+                if (settled) return true;
+                settled = true;
+                if (!warp_all(mbar_wait(&bars->pdone[x], (n_x - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag))) return false;
+                tc_fence_after();
+                return true;
+            };
             float s[TILE];
             uint32_t w[32];
             if (warp_on) {
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * h));
-                // O_x is complete up to the last step (its product precedes these scores)
+                tmem_wait_ld();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(&bars->sfree[buf], arrivals);
+            if (warp_on) {
                 if (__any_sync(0xffffffffu, m_next != m)) {
+                    if (!settle()) return;
                     const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_next);
                     l *= a;
                     rescale<D>(to, a);
                     m = m_next;
                 }
-                tmem_wait_ld();
                 if (negate) {
 #pragma unroll
                     for (int e = 0; e < TILE; ++e) s[e] = -s[e];
@@ -671,6 +651,7 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
                 if (__any_sync(0xffffffffu, tm > m + LIMIT)) {
                     const float m_new = fmaxf(m, tm);
                     if (i != first) {
+                        if (!settle()) return;
                         const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_new);
                         l *= a;
                         rescale<D>(to, a);
@@ -680,15 +661,18 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
                 }
                 m_next = tm > m + RESCALE ? tm : m;
                 l += lsum;
-                tmem_st32(ts, w);
+                if (!settle()) return;
+                tmem_st32(tp, w);
                 tmem_wait_st();
                 tc_fence_before();
+            } else if (!settle()) {
+                return;      // (or its arrivals would count for the step before)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_n(&bars->pready[x][0], arrivals);
             if (warp_on) {
                 l += weights64(s + 64, cs, m, w);
-                tmem_st32(ts + 32, w);
+                tmem_st32(tp + 32, w);
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -698,14 +682,8 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
         // ---- the piece's partial: O / l and log2 of the sum
         const bool took = first < pc.steps;
         if (took) {
-            if (!warp_all(mbar_wait(&bars->odone[x], pieces & 1u, FLAG_MMA_WAIT, c.abort_flag))) return;
-            ++pieces;
+            if (!warp_all(mbar_wait(&bars->pdone[x], (n_x - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag))) return;
             tc_fence_after();
-            if (releases) {
-                const int last = first + ((pc.steps - 1 - first) & ~1);
-                const uint32_t nv = 2 * (k.tiles + (uint32_t)(pc.two ? last >> 1 : last)) + 1;
-                mbar_arrive_n(&bars->empty[nv % C::NS], use);
-            }
         }
         if (warp_on) {
             const bool on = r < rows;
@@ -722,25 +700,30 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
                 // prefix rows next to each other, so that a warp stores whole lines; a suffix's few
                 // rows each by itself
                 float *dst = pc.prefix ? p.o_p + at * D * ROWS + r : p.o_s + (at * rs + r) * D;
-                uint32_t o[D];
 #pragma unroll
-                for (int d = 0; d < D; d += 32) tmem_ld32(to + d, *reinterpret_cast<uint32_t(*)[32]>(o + d));
-                tmem_wait_ld();
-                if (on && pc.prefix) {
+                for (int d0 = 0; d0 < D; d0 += 64) {
+                    uint32_t o[64];
+                    tmem_ld32(to + d0, *reinterpret_cast<uint32_t(*)[32]>(o));
+                    tmem_ld32(to + d0 + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+                    tmem_wait_ld();
+                    if (d0 + 64 == D) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_n(&bars->ofree[x], arrivals);
+                    }
+                    if (on && pc.prefix) {
 #pragma unroll
-                    for (int d = 0; d < D; ++d) dst[d * ROWS] = __uint_as_float(o[d]) * inv;
-                } else if (on) {
+                        for (int d = 0; d < 64; ++d) dst[(d0 + d) * ROWS] = __uint_as_float(o[d]) * inv;
+                    } else if (on) {
 #pragma unroll
-                    for (int d = 0; d < D; d += 4)
-                        *reinterpret_cast<float4 *>(dst + d) =
-                            make_float4(__uint_as_float(o[d]) * inv, __uint_as_float(o[d + 1]) * inv,
-                                        __uint_as_float(o[d + 2]) * inv, __uint_as_float(o[d + 3]) * inv);
+                        for (int d = 0; d < 64; d += 4)
+                            *reinterpret_cast<float4 *>(dst + d0 + d) =
+                                make_float4(__uint_as_float(o[d]) * inv, __uint_as_float(o[d + 1]) * inv,
+                                            __uint_as_float(o[d + 2]) * inv, __uint_as_float(o[d + 3]) * inv);
+                    }
                 }
-                tc_fence_before();
             }
-        }
-        if (took) {
-            __syncwarp();
+        } else if (took) {
             if (lane == 0) mbar_arrive_n(&bars->ofree[x], arrivals);
         }
     }
@@ -764,16 +747,16 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
     if (tid == 0) {
         for (uint32_t s = 0; s < C::NS; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 2);
+            mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->qfull[i], 1);
-            mbar_init(&bars->qempty[i], 2);
+            mbar_init(&bars->qempty[i], 1);
             mbar_init(&bars->sready[i], 1);
             mbar_init(&bars->pready[i][0], 4);
             mbar_init(&bars->pready[i][1], 4);
-            mbar_init(&bars->turn[i], 1);
-            mbar_init(&bars->odone[i], 1);
+            mbar_init(&bars->sfree[i], 4);
+            mbar_init(&bars->pdone[i], 1);
             mbar_init(&bars->ofree[i], 4);
         }
         bars->abort_flag = 0;
@@ -815,7 +798,8 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
     if (warp < 4) {
         regs_dec<REGS_CTRL>();
         if (warp == 0 && lane == 0) producer<D>(p, &kp, &vp, &ks, &vs, &qm, c);
-        if ((warp == 1 || warp == 2) && lane == 0) mma_issuer<D>(p, c, warp - 1);
+        if (warp == 1 && lane == 0) score_issuer<D>(p, c);
+        if (warp == 2 && lane == 0) value_issuer<D>(p, c);
     } else {
         regs_inc<REGS_SOFT>();
         softmax_group<D>(p, c, warp, lane);
