@@ -16,45 +16,54 @@
 // Work.  A unit is (KV head, pair of 128-row tiles) over the prefix, or (sequence, KV head)
 // over a suffix; each unit is a run of 128-token K/V tiles.  All units are laid end to end on a
 // line whose positions stand for time -- WP2 a prefix tile that serves two row tiles, WP1 one that
-// serves one, WS a suffix tile, and one tile more for each unit, whose start and end cost about
-// that -- and worker w (one CTA per SM) takes an equal contiguous range of it, computed on
-// the device from prefix_len and seq_lens (so a captured call may be replayed with other
-// lengths).  Prefix and suffix work thus run side by side: some SMs keep the tensor cores busy
-// while others stream suffixes from memory.  Every piece (a worker's part of a unit) leaves a
-// normalised partial and its log-sum-exp in the caller's workspace; prefix_merge_kernel joins a
-// row's partials.
+// serves one, WS a suffix tile, and for a unit's start and end one tile more (prefix) or US (suffix)
+// -- and worker w (one CTA per SM) takes an equal contiguous range of it, computed on the device
+// from prefix_len and seq_lens (so a captured call may be replayed with other lengths).  Prefix and
+// suffix work thus run side by side: some SMs keep the tensor cores busy while others stream
+// suffixes from memory.  The weights are measured: with 4, 2, 4 and one tile a unit (8, 4, 8 and 1
+// in these positions) 64 sequences behind 32768 tokens took 151 us and 16 of up to 4096 tokens
+// 108 us; with 8, 6, 6 and 3 they took 141 and 83 us.  Every piece (a worker's part of a unit)
+// leaves a normalised partial and its log-sum-exp in the caller's workspace; prefix_merge_kernel
+// joins a row's partials.
 //
 // Pipeline of a CTA (384 threads):
-//   warp 0       producer: TMA loads (128-byte swizzle, no multicast) of Q tiles and of K and
-//                V tiles into a ring.
-//   warps 1, 2   one thread each issues the tcgen05.mma of group x = 0, 1: S_x = Q K^T (A, B from
-//                shared memory) and O_x += P_x V (P_x read from tensor memory, V tile MN-major).
+//   warp 0       producer: TMA loads (128-byte swizzle, no multicast) of Q tiles, and of K and
+//                V tiles into a ring each.
+//   warp 1       one thread issues the tcgen05.mma of the scores, S = Q K^T (A, B from shared memory).
+//   warp 2       one thread issues those of the outputs, O_x += P_x V (P_x read from tensor memory,
+//                V tile MN-major).
 //   warps 4..11  two softmax groups x = 0, 1 of 128 threads, one thread per row: a row's 128
-//                scores are one TMEM lane, so its maximum and sum need no exchange.  P_x (bf16)
-//                overwrites S_x.  They also release the K, V and Q tiles, since the commit that
-//                announces scores tells them that the products before are done.
+//                scores are one TMEM lane, so its maximum and sum need no exchange.
 // Steps alternate between the groups, so that one group's exponentials run while the tensor
 // cores work for the other: in a two-row-tile unit the groups hold the two row tiles and
 // each K/V tile makes two steps; in a one-row-tile unit both groups hold the same rows and take
 // alternate K/V tiles, each with its own (max, sum, O), which the merge joins.
 //
-// A group's step is a chain: scores, exponentials, weights times V, next scores (tensor memory
-// has no room for a second score buffer), so its length bounds the kernel.  Two things shorten it.
+// Tensor memory holds O_0, O_1 (D columns each), P_0, P_1 (64 each, bf16) and, in what is left, one
+// score buffer that the groups use in turn (D = 128) or two (D = 64).  A score buffer is free as soon
+// as its scores are in registers, so the next step's scores are computed under this step's
+// exponentials, which then follow one another without a wait.  Two more things keep them so.
 // The weights are taken against the running maximum of the steps before, so no exponential waits
 // for this step's; the maximum moves afterwards, when a row's scores have exceeded it by more
 // than 2^8 (its O and sum are then rescaled before the next step's product), and at once only on
 // a piece's first step and where they exceed it by 2^LIMIT.  And the weights are handed over in two
 // halves of 64 tokens, the first half's product running under the second half's exponentials.
 // Measured on 64 sequences of 64 heads behind 32768 tokens, cycles a pair of steps (the products
-// alone: 2048):
-//   one issuer for both groups                6200  eight MMAs take ~600 to issue, a commit ~180
-//   an issuer a group, issuing freely         5500  the groups' products interleave, both end late,
-//                                                   and the groups fall into step
-//   ... in turns                              4250
-//   steps in halves, a score buffer each      3900  the score products of N = 64 are bound by shared
-//                                                   memory, which also takes the TMA writes
-//   two threads a row                         4400  a swap of maxima, and registers that do not reach
-// Weights enter the value product rounded to bf16 (half a step, 2^-9 relative, each independent
+// alone: 2048, the exponentials alone: 2048):
+//   weights over their scores, one issuer       6200  eight MMAs take ~600 to issue, a commit ~180
+//   ... an issuer a group, issuing freely       5500  the groups' products interleave, both end late,
+//                                                     and the groups fall into step
+//   ... in turns                                4700
+//   ... steps in halves, a score buffer each    4300  the score products of N = 64 are bound by shared
+//                                                     memory, which also takes the TMA writes
+//   ... two threads a row                       4900  a swap of maxima, and registers that do not reach
+//   weights apart, an issuer a product          4000  (this kernel)
+// What bounds it now is the softmax warps: two a scheduler, each 1300-1500 cycles for 64 columns
+// when both run (the exponential unit's share is 1024), and 250-400 at each of four hand-overs.
+// Asking for the barriers' phases ahead of their use changed nothing.  A suffix is bound by
+// memory where it is long (4.2 TB/s at 8 sequences of up to 8000 tokens behind 32768) and by the
+// start and end of a piece, some 5000 cycles, where it is short.
+// Weights enter the value product rounded to bf16 (at most half a step, 2^-8 relative, each independent
 // of the others; the output is rounded to bf16 itself); sums, maxima and O are fp32.
 #pragma once
 #include "common.cuh"
@@ -134,7 +143,10 @@ struct Cfg {
     static constexpr int NCH = D / 64;                  // 64-wide chunks of a row
     static constexpr int KV_BYTES = NCH * CHUNK;        // a K or V tile
     static constexpr int Q_BYTES = NCH * CHUNK;         // a Q tile
-    static constexpr uint32_t NS = (160 * 1024) / KV_BYTES;   // ring slots (K and V tiles alternate)
+    // Slots: a ring of K tiles and one of V tiles.  (In one ring with an odd number of slots the
+    // score issuer, which waits for K tiles alone, could be a use of the slot behind and take its
+    // barrier's parity for the next one's.)
+    static constexpr uint32_t NS = (160 * 1024) / KV_BYTES, NK = NS / 2, NV = NS - NK;
     static constexpr int OFF_Q = NS * KV_BYTES;
     static constexpr int OFF_BARS = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_TABLE = OFF_BARS + 384;
@@ -187,6 +199,7 @@ struct Bars {
     uint64_t pready[2][2];   // [group][half] the weights are written (and O_x rescaled)
     uint64_t pdone[2];       // group x's value product is done
     uint64_t ofree[2];       // group x has read O_x
+    uint64_t drain[2];       // an issuer's products after a wait that gave up
     uint32_t tmem;
     int prefix_len;
     int abort_flag;
@@ -385,7 +398,7 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
     using C = Cfg<D>;
     Bars *bars = c.bars;
     const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
-    uint32_t n = 0;                 // tiles (K and V) issued
+    uint32_t n[2] = {0, 0};         // K and V tiles issued
     bool ok = true;
     Walk k = walk_start(c.line, c.w);
     while (ok && walk_next(k, p, c.line, c.tab, c.prefix_len, c.w)) {
@@ -413,12 +426,13 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
                                           : tile_source(p.block_table, p.max_pages, p.page_size, pc.b, lt, TILE, pc.len);
             const int z = src.page * p.n_kv + pc.j;
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-                const uint32_t s = n % C::NS;
-                if (!mbar_wait(&bars->empty[s], ((n / C::NS) & 1u) ^ 1u, FLAG_EMPTY_WAIT, c.abort_flag)) {
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t ring = kv ? C::NV : C::NK, s = (kv ? C::NK : 0) + n[kv] % ring;
+                if (!ok || !mbar_wait(&bars->empty[s], ((n[kv] / ring) & 1u) ^ 1u, FLAG_EMPTY_WAIT, c.abort_flag)) {
                     ok = false;
                     break;
                 }
+                ++n[kv];
                 mbar_arrive_expect_tx(&bars->full[s], C::KV_BYTES);
 #pragma unroll
                 for (int ch = 0; ch < C::NCH; ++ch)
@@ -429,8 +443,12 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
     }
     if (!ok) {
         // Let every copy already issued land before the CTA can exit.
-        for (uint32_t m = n > C::NS ? n - C::NS : 0; m < n; ++m)
-            mbar_wait_sleep(&bars->full[m % C::NS], (m / C::NS) & 1u, FLAG_FULL_WAIT, nullptr);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t ring = kv ? C::NV : C::NK, base = kv ? C::NK : 0;
+            for (uint32_t m = n[kv] > ring ? n[kv] - ring : 0; m < n[kv]; ++m)
+                mbar_wait_sleep(&bars->full[base + m % ring], (m / ring) & 1u, FLAG_FULL_WAIT, nullptr);
+        }
         if (k.quse0 > 0) mbar_wait_sleep(&bars->qfull[0], (k.quse0 - 1) & 1u, FLAG_FULL_WAIT, nullptr);
         if (k.quse1 > 0) mbar_wait_sleep(&bars->qfull[1], (k.quse1 - 1) & 1u, FLAG_FULL_WAIT, nullptr);
     }
@@ -441,7 +459,7 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
 // last products.
 // S = Q K^T of every step, into the score buffers in turn.
 template <int D>
-__device__ __forceinline__ void score_issuer(const PrefixParams &p, const Ctx &c) {
+__device__ __forceinline__ bool score_issuer(const PrefixParams &p, const Ctx &c) {
     using C = Cfg<D>;
     constexpr uint32_t NSB = Tm<D>::NSB;
     Bars *bars = c.bars;
@@ -455,12 +473,12 @@ __device__ __forceinline__ void score_issuer(const PrefixParams &p, const Ctx &c
         for (int i = 0; i < pc.steps; ++i, ++n) {
             const uint32_t x = n & 1u, buf = n % NSB;
             const int qslot = pc.two ? (k.qs + i) & 1 : k.qs;
-            const uint32_t nk = 2 * (k.tiles + (uint32_t)(pc.two ? i >> 1 : i)), slot = nk % C::NS;
+            const uint32_t t = k.tiles + (uint32_t)(pc.two ? i >> 1 : i), slot = t % C::NK;
             if (i < (pc.two ? 2 : 1) &&
                 !mbar_wait(&bars->qfull[qslot], ((qslot ? k.quse1 : k.quse0) - 1) & 1u, FLAG_FULL_WAIT, c.abort_flag))
-                return;
-            if (!mbar_wait(&bars->full[slot], (nk / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
-            if (n >= NSB && !mbar_wait(&bars->sfree[buf], (n / NSB - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
+                return false;
+            if (!mbar_wait(&bars->full[slot], (t / C::NK) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return false;
+            if (n >= NSB && !mbar_wait(&bars->sfree[buf], (n / NSB - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return false;
             tc_fence_after();
             const uint32_t ts = bars->tmem + Tm<D>::S + 128 * buf;
             const uint32_t q = desc_lo(smem + C::OFF_Q + qslot * C::Q_BYTES - (!pc.prefix && x == 1 ? qoff_suffix : 0), 16);
@@ -476,10 +494,11 @@ __device__ __forceinline__ void score_issuer(const PrefixParams &p, const Ctx &c
             if (i + (pc.two ? 2 : 1) >= pc.steps) umma_commit(&bars->qempty[qslot]);
         }
     }
+    return true;
 }
 // O_x += P_x V of every step, each in two halves of 64 tokens as the weights come.
 template <int D>
-__device__ __forceinline__ void value_issuer(const PrefixParams &p, const Ctx &c) {
+__device__ __forceinline__ bool value_issuer(const PrefixParams &p, const Ctx &c) {
     using C = Cfg<D>;
     Bars *bars = c.bars;
     const uint32_t smem = smem_u32(c.smem);
@@ -490,21 +509,21 @@ __device__ __forceinline__ void value_issuer(const PrefixParams &p, const Ctx &c
         const Piece &pc = k.pc;
         for (int i = 0; i < pc.steps; ++i, ++n) {
             const uint32_t x = n & 1u, par = (n >> 1) & 1u;
-            const uint32_t nv = 2 * (k.tiles + (uint32_t)(pc.two ? i >> 1 : i)) + 1, slot = nv % C::NS;
-            if (!mbar_wait(&bars->full[slot], (nv / C::NS) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return;
+            const uint32_t t = k.tiles + (uint32_t)(pc.two ? i >> 1 : i), slot = C::NK + t % C::NV;
+            if (!mbar_wait(&bars->full[slot], (t / C::NV) & 1u, FLAG_FULL_WAIT, c.abort_flag)) return false;
             if (i < 2) {
                 const uint32_t before = x ? pieces[1]++ : pieces[0]++;
-                if (before > 0 && !mbar_wait(&bars->ofree[x], (before - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return;
+                if (before > 0 && !mbar_wait(&bars->ofree[x], (before - 1) & 1u, FLAG_MMA_WAIT, c.abort_flag)) return false;
             }
             const uint32_t tp = bars->tmem + Tm<D>::P + 64 * x, to = bars->tmem + Tm<D>::O + D * x;
             const uint32_t vt = desc_lo(smem + slot * C::KV_BYTES, CHUNK);
-            if (!mbar_wait(&bars->pready[x][0], par, FLAG_MMA_WAIT, c.abort_flag)) return;
+            if (!mbar_wait(&bars->pready[x][0], par, FLAG_MMA_WAIT, c.abort_flag)) return false;
             tc_fence_after();
             if (i < 2) mma_ts<false>(to, tp, vt, idesc);
             else mma_ts<true>(to, tp, vt, idesc);
 #pragma unroll
             for (int kk = 1; kk < TILE / 32; ++kk) mma_ts<true>(to, tp + kk * 8, vt + kk * (2048 >> 4), idesc);
-            if (!mbar_wait(&bars->pready[x][1], par, FLAG_MMA_WAIT, c.abort_flag)) return;
+            if (!mbar_wait(&bars->pready[x][1], par, FLAG_MMA_WAIT, c.abort_flag)) return false;
             tc_fence_after();
 #pragma unroll
             for (int kk = TILE / 32; kk < TILE / 16; ++kk) mma_ts<true>(to, tp + kk * 8, vt + kk * (2048 >> 4), idesc);
@@ -512,6 +531,7 @@ __device__ __forceinline__ void value_issuer(const PrefixParams &p, const Ctx &c
             umma_commit(&bars->pdone[x]);
         }
     }
+    return true;
 }
 
 // ------------------------------------------------------------------ softmax (warps 4..11)
@@ -758,6 +778,7 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
             mbar_init(&bars->sfree[i], 4);
             mbar_init(&bars->pdone[i], 1);
             mbar_init(&bars->ofree[i], 4);
+            mbar_init(&bars->drain[i], 1);
         }
         bars->abort_flag = 0;
         fence_mbar_init();
@@ -798,8 +819,11 @@ prefix_decode_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap k
     if (warp < 4) {
         regs_dec<REGS_CTRL>();
         if (warp == 0 && lane == 0) producer<D>(p, &kp, &vp, &ks, &vs, &qm, c);
-        if (warp == 1 && lane == 0) score_issuer<D>(p, c);
-        if (warp == 2 && lane == 0) value_issuer<D>(p, c);
+        // (an issuer that gave up lets its products in flight end before the CTA can)
+        if ((warp == 1 || warp == 2) && lane == 0 && !(warp == 1 ? score_issuer<D>(p, c) : value_issuer<D>(p, c))) {
+            umma_commit(&bars->drain[warp - 1]);
+            mbar_wait_sleep(&bars->drain[warp - 1], 0, FLAG_MMA_WAIT, nullptr);
+        }
     } else {
         regs_inc<REGS_SOFT>();
         softmax_group<D>(p, c, warp, lane);
