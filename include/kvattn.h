@@ -19,8 +19,14 @@
  *    value up-projection is applied by the caller).  ("Attention variants: MQA, GQA,
  *    and MLA", section "MLA: cache a latent, not the keys and values".)
  *
+ * For serving there are, besides (documented at their declarations): a cache written with a
+ * scale per row, its read back and the decode over it (kvattn_rope_append_rowscale,
+ * kvattn_gather_rowscale, kvattn_gqa_decode_rowscale), decode of a batch behind a shared
+ * prefix (kvattn_gqa_decode_prefix), and the verification of drafted tokens
+ * (kvattn_verify_drafts).
+ *
  * For each sequence b and query head h, with T = seq_lens[b] and scaled scores
- * s_t (t < T), both entry points write
+ * s_t (t < T), the two forms write
  *      out[b, h, :] = sum_t softmax(s)_t * value_t       (fp32)
  *      lse[b, h]    = log(sum_t exp(s_t))                 (fp32, natural log)
  * An empty sequence (T == 0) gives out = 0 and lse = -inf.
@@ -412,12 +418,15 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
  *                a contiguous cache, one page a sequence (num_pages = batch,
  *                max_pages_per_seq = 1, page_size = the capacity)
  *   out          device bf16 [batch, q_len, n_q_heads, head_dim], rounded once: the type the
- *                output projection reads, and what the weights' two E4M3 parts (~8 significant
- *                bits) support;  lse fp32 [batch, q_len, n_q_heads]
+ *                output projection reads;  lse fp32 [batch, q_len, n_q_heads]
+ * The codes and the query enter the tensor-core products in f16 (the codes exactly, the query
+ * times a power of two), the softmax weights times their token's value scale in f16 relative to
+ * the unit's largest (11 significant bits); accumulation is fp32.
  * head_dim 128, n_q_heads / n_kv_heads <= 64, page_size a multiple of 128 (paged); batch *
  * q_len <= 4096.  Scales from 2^-60 to 2^60 keep full precision.  Codes and scales past a
  * sequence's length are never read into a result; everything else as for
- * kvattn_gqa_decode_fp8.
+ * kvattn_gqa_decode_fp8.  With q_len > 1 a new token's value scale has to be finite also for the
+ * older new tokens, which give it weight zero.
  */
 int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales,
                                const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, int num_pages,
@@ -531,8 +540,9 @@ int kvattn_clear_device_flags(void);
  * Kernels this library has launched (enqueued successfully) from the calling host thread
  * since the library was loaded: a decode call adds one (the decode kernel), or two when a
  * combine kernel merges units cut between workers, plus one when several new tokens run
- * as a virtual batch; an append adds one.  Read it before and after a call to count that
- * call's kernels.
+ * as a virtual batch; an append, a read back and a verification add one; a prefix decode adds
+ * two (decode and merge), or three where the batch is above 640 sequences.  Read it before and
+ * after a call to count that call's kernels.
  */
 unsigned long long kvattn_kernel_launches(void);
 

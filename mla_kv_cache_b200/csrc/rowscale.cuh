@@ -39,7 +39,7 @@ constexpr int kRowThreads = 128;
 // cos and sin of position * base^(-2i/d) for pair i.  The angle is formed in turns in fp64
 // (a position of 10^6 leaves it good to ~1e-10 of a turn) and only its fraction of a turn is
 // taken to fp32, so no reduction of a large argument is left to the fp32 functions; their
-// results are off by ~2e-7 at most, against 2^-9 of the bf16 rounding and 2^-4 of E4M3.  A pair's
+// results are off by ~2e-7 at most, against 2^-8 of the bf16 rounding and 2^-4 of E4M3.  A pair's
 // turns per position are a product of two of the 24 powers that come with the launch.
 __device__ __forceinline__ float2 rope_turn(const RowAppendParams &p, int pos, int i) {
     const double turns = (double)pos * (p.turn_hi[i >> 4] * p.turn_lo[i & 15]);

@@ -58,7 +58,8 @@ def out_bound(ref, p, v, slack, fmt):
     bf16 weights: half a step each.  E4M3 weights in two parts: the remainder's half step of a
     remainder of at most a half step (2^-8), or, where the parts run out of range, the smallest
     half step 2^-10 of weights that reach at least 2^4 of 2^6 (the lazy maximum moves after a
-    factor of 4): 2^-14 of the largest weighted row, never more than the weight itself."""
+    factor of 4): 2^-14 of the largest weighted row, never more than the weight itself.  (Weights
+    in f16, half a step 2^-12 and 2^-25 absolute of weights that reach at least 2^0, lie within.)"""
     p = p.double()
     v = v.double().abs()
     w = p @ v
