@@ -423,7 +423,8 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
  * times a power of two), the softmax weights times their token's value scale in f16 relative to
  * the unit's largest (11 significant bits); accumulation is fp32.
  * head_dim 128, n_q_heads / n_kv_heads <= 64, page_size a multiple of 128 (paged); batch *
- * q_len <= 4096.  Scales from 2^-60 to 2^60 keep full precision.  Codes and scales past a
+ * q_len <= 4096.  A page outside the pool reads as rows of zeros.  Scales from 2^-60 to 2^60
+ * keep full precision.  Codes and scales past a
  * sequence's length are never read into a result; everything else as for
  * kvattn_gqa_decode_fp8.  With q_len > 1 a new token's value scale has to be finite also for the
  * older new tokens, which give it weight zero.

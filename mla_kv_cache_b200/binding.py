@@ -928,8 +928,8 @@ def kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sa
     """Verification of drafted tokens (include/kvattn.h, kvattn_verify_drafts): target_probs
     [B, L + 1, V] fp32 or bf16, draft_probs [B, L, V] of the same type (None: point drafts),
     draft_tokens [B, L] int32, u_accept [B, L] and u_sample [B] fp32, draft_lens [B] int32 or
-    None.  Rows may be strided (a padded vocabulary).  Returns (accepted [B], tokens [B, L + 1])
-    int32."""
+    None.  With L = 0 (a plain draw) draft_tokens and u_accept may be None.  Rows may be strided
+    (a padded vocabulary).  Returns (accepted [B], tokens [B, L + 1]) int32."""
     import torch
     dtype = target_probs.dtype
     if dtype is not torch.float32 and dtype is not torch.bfloat16:
@@ -950,8 +950,9 @@ def kvattn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sa
         accepted = torch.empty((B,), dtype=i32, device=target_probs.device)
     if tokens is None:
         tokens = torch.empty((B, L1), dtype=i32, device=target_probs.device)
-    rc = lib().kvattn_verify_drafts(pa, qa, _at(draft_tokens, "draft_tokens", i32, (B, L), ix), lens,
-                                    _at(u_accept, "u_accept", f32, (B, L), ix), _at(u_sample, "u_sample", f32, (B,), ix),
+    drafts = None if L == 0 and draft_tokens is None else _at(draft_tokens, "draft_tokens", i32, (B, L), ix)
+    u = None if L == 0 and u_accept is None else _at(u_accept, "u_accept", f32, (B, L), ix)
+    rc = lib().kvattn_verify_drafts(pa, qa, drafts, lens, u, _at(u_sample, "u_sample", f32, (B,), ix),
                                     _at(accepted, "accepted", i32, (B,), ix), _at(tokens, "tokens", i32, (B, L1), ix), B, L,
                                     V, 1 if dtype is torch.bfloat16 else 0, pb, pl, qb, ql, _raw_stream(ix))
     if rc != KVATTN_OK:

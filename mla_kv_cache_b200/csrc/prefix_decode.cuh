@@ -85,6 +85,7 @@ struct PrefixParams {
     int B, L, n_q, n_kv, g;
     int P_max, T_max;              // capacities (lengths are clamped to them)
     int prefix_page, page_size;    // rows per page of the prefix's and the suffixes' cache
+    int prefix_pages, pages;       // pages of the two (one pool when paged)
     int max_pages;                 // block_table columns
     int tok_tile;                  // new tokens in a row tile: floor(128 / g)
     int row_tiles, pairs;          // ceil(B L / tok_tile), ceil(row_tiles / 2)
@@ -424,7 +425,9 @@ __device__ __forceinline__ void producer(const PrefixParams &p, const CUtensorMa
         for (int lt = pc.lt0; lt < pc.lt1 && ok; ++lt) {
             const TileSrc src = pc.prefix ? tile_source(p.prefix_table, 0, p.prefix_page, 0, lt, TILE, pc.len)
                                           : tile_source(p.block_table, p.max_pages, p.page_size, pc.b, lt, TILE, pc.len);
-            const int z = src.page * p.n_kv + pc.j;
+            // (a page outside the pool is read as zeros: a coordinate outside the map)
+            const bool inside = src.page >= 0 && src.page < (pc.prefix ? p.prefix_pages : p.pages);
+            const int z = inside ? src.page * p.n_kv + pc.j : -1;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t ring = kv ? C::NV : C::NK, s = (kv ? C::NK : 0) + n[kv] % ring;

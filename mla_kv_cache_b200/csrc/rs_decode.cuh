@@ -183,7 +183,8 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
                 if (!mbar_wait(&bars->empty[s], ((uint32_t)(k / NST) & 1u) ^ 1u, FLAG_EMPTY_WAIT, abort_flag)) { ok = false; break; }
                 mbar_arrive_expect_tx(&bars->full[s], STAGE);
                 const TileSrc src = tile_source(p.block_table, p.max_pages, p.page_size, pc.b, lt, TILE, len, start);
-                const int z = src.page * p.n_kv + pc.i;
+                // (a page outside the pool is read as zeros: a coordinate outside the map)
+                const int z = src.page >= 0 && src.page < p.pages ? src.page * p.n_kv + pc.i : -1;
                 uint8_t *st = smem + s * STAGE;
                 // (the maps see a row of 128 codes as 64 two-byte elements)
                 tma_load_3d(st, &kmap, &bars->full[s], 0, src.y, z, pol);

@@ -127,6 +127,7 @@ int prefix_entry(const uint16_t *q, const uint16_t *kp, const uint16_t *vp, cons
         snprintf(t_detail, sizeof(t_detail), "workspace of %zu B, %zu needed", workspace_bytes, w.bytes);
         return KVATTN_ERR_INVALID_ARG;
     }
+    if (4ll * w.row_tiles * n_kv >= (1ll << 31)) return KVATTN_ERR_UNSUPPORTED;
     const int g = n_q / n_kv;
     CUtensorMap maps[5];
     const void *base[4] = {kp, vp, ks, vs};
@@ -161,6 +162,8 @@ int prefix_entry(const uint16_t *q, const uint16_t *kp, const uint16_t *vp, cons
     p.T_max = max_seq_len;
     p.prefix_page = prefix_page;
     p.page_size = page_size;
+    p.prefix_pages = (int)prefix_pages;
+    p.pages = (int)pages;
     p.max_pages = max_pages;
     p.tok_tile = w.tok_tile;
     p.row_tiles = w.row_tiles;
