@@ -81,8 +81,10 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
 template <int LPR>
 __global__ void __launch_bounds__(kRowThreads) row_append_kernel(const __grid_constant__ RowAppendParams p) {
     constexpr int RPW = 32 / LPR;                // rows the warp handles at once
-    constexpr int U = 1;                         // of these in flight (more cost registers: 18.1 us with 2 for
-                                                 // 8192 tokens of 8 + 2 * 8 heads of 64, 14.1 with 1)
+    // Of these in flight: two of the queries (8192 tokens of 64 + 2 * 8 heads of 128: 57.3 us, 58.5 with
+    // one), one of the keys or values (two cost registers: 17.3 us for 8192 tokens of 8 + 2 * 8 heads of 64,
+    // 14.3 with one, against 7.4 and 8.5 for 700 of the former).
+    constexpr int UQ = 2, U = 1;
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int n = (int)(item / p.parts), part = (int)(item - (long long)n * p.parts);
@@ -138,15 +140,15 @@ __global__ void __launch_bounds__(kRowThreads) row_append_kernel(const __grid_co
     if (r0 < q1) {
         const __nv_bfloat16 *src = p.q + (long long)n * p.q_stride;
         __nv_bfloat16 *dst = p.q_out + (long long)n * p.q_out_stride;
-        for (int base = r0; base < q1; base += RPW * U) {
-            RowHalves x[U];
+        for (int base = r0; base < q1; base += RPW * UQ) {
+            RowHalves x[UQ];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < UQ; ++u) {
                 const int r = base + u * RPW + sub;
                 if (r < q1) x[u] = load(src + r * p.d);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < UQ; ++u) {
                 const int r = base + u * RPW + sub;
                 if (r >= q1 || !lane_on) continue;
                 if (p.rotate) {
