@@ -16,13 +16,15 @@
 // Work.  A unit is (KV head, pair of 128-row tiles) over the prefix, or (sequence, KV head)
 // over a suffix; each unit is a run of 128-token K/V tiles.  All units are laid end to end on a
 // line whose positions stand for time -- WP2 a prefix tile that serves two row tiles, WP1 one that
-// serves one, WS a suffix tile, and for a unit's start and end one tile more (prefix) or US (suffix)
-// -- and worker w (one CTA per SM) takes an equal contiguous range of it, computed on the device
+// serves one, WS a suffix tile, and for a unit's start and end UP2, UP1 or US tiles more -- and worker w (one CTA per SM) takes an equal contiguous range of it, computed on the device
 // from prefix_len and seq_lens (so a captured call may be replayed with other lengths).  Prefix and
 // suffix work thus run side by side: some SMs keep the tensor cores busy while others stream
 // suffixes from memory.  The weights are measured: with 4, 2, 4 and one tile a unit (8, 4, 8 and 1
 // in these positions) 64 sequences behind 32768 tokens took 151 us and 16 of up to 4096 tokens
-// 108 us; with 8, 6, 6 and 3 they took 141 and 83 us.  Every piece (a worker's part of a unit)
+// 108 us; with 8, 6, 6 and one, one and three tiles they took 141 and 83 us.  A prefix unit of two row
+// tiles that counts for one tile more leaves its workers behind where it is short (128 sequences of
+// up to 64 behind 1000 tokens 89 us, 62 with four; of up to 300 behind 300 99 and 78 us); one of a
+// single row tile does not (8 sequences behind 2000 tokens 18.7 us, 20.2 with four).  Every piece (a worker's part of a unit)
 // leaves a normalised partial and its log-sum-exp in the caller's workspace; prefix_merge_kernel
 // joins a row's partials.
 //
@@ -108,7 +110,7 @@ constexpr int CHUNK = 128 * 128;          // [128 rows x 128 bytes]
 constexpr int NS_MAX = 10;
 constexpr float RESCALE = 8.f, LIMIT = 64.f;
 // Line positions (see above), and the least a worker takes.
-constexpr uint32_t WP2 = 8, WP1 = 6, WS = 6, US = 3, W_MIN = 8;
+constexpr uint32_t WP2 = 8, WP1 = 6, WS = 6, UP2 = 4, UP1 = 1, US = 3, W_MIN = 8;
 constexpr long long LINE_LIMIT = 1ll << 30;
 
 // Two fp32 values in one 64-bit register pair: one instruction works on both.
@@ -256,7 +258,7 @@ __device__ __forceinline__ Line make_line(const PrefixParams &p, uint32_t n_p, u
     Line l;
     l.n_p = n_p;
     l.wp = p.row_tiles > 1 ? WP2 : WP1;
-    l.unit_p = n_p ? (n_p + 1) * l.wp : 0;
+    l.unit_p = n_p ? (n_p + (p.row_tiles > 1 ? UP2 : UP1)) * l.wp : 0;
     l.p_total = (uint32_t)(p.n_kv * p.pairs) * l.unit_p;
     l.total = l.p_total + suffix_units * (uint32_t)p.n_kv * WS;
     l.W = (l.total + p.workers - 1) / p.workers;

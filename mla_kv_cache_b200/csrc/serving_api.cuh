@@ -61,7 +61,7 @@ PrefixPlan prefix_plan(const DeviceState *dev, int B, int L, int n_q, int n_kv, 
     w.pairs = (w.row_tiles + 1) / 2;
     const long long tiles_p = (P_max + pfx::TILE - 1) / pfx::TILE, tiles_s = (T_max + pfx::TILE - 1) / pfx::TILE;
     const long long units_p = (long long)n_kv * w.pairs, units_s = (long long)B * n_kv;
-    w.line = units_p * (tiles_p + 1) * (w.row_tiles > 1 ? pfx::WP2 : pfx::WP1) + units_s * (tiles_s + pfx::US) * pfx::WS;
+    w.line = (w.row_tiles > 1 ? units_p * (tiles_p + pfx::UP2) * pfx::WP2 : units_p * (tiles_p + pfx::UP1) * pfx::WP1) + units_s * (tiles_s + pfx::US) * pfx::WS;
     long long workers = g_force_workers > 0 ? g_force_workers : dev->sms;
     const long long most = (w.line + pfx::W_MIN - 1) / pfx::W_MIN;
     if (workers > most) workers = most;
