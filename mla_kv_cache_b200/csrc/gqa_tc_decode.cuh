@@ -590,7 +590,7 @@ __device__ __forceinline__ void softmax_warps(const GqaParams &p, const Ctx &c, 
                 if (in_tile) {
                     for (int qi = 0; qi < p.q_len; ++qi) {
                         const int hi = len - p.q_len + qi + 1;
-                        const int lo = p.window > 0 ? hi - p.window : 0;
+                        const int lo = p.window > 0 ? window_start(hi, p.window) : 0;
                         if (posr < hi && posr >= lo) vis |= group_bits << (qi * p.g);
                     }
                 }

@@ -320,7 +320,7 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
                 qa[kk][2 + h] = pack_f16x2(bf16_lo(raw[h][kk].y) * up, bf16_hi(raw[h][kk].y) * up);
             }
             hi[h] = len - p.q_len + row_qi[h] + 1;
-            lo[h] = p.window > 0 ? hi[h] - p.window : 0;
+            lo[h] = p.window > 0 ? window_start(hi[h], p.window) : 0;
         }
         // no mask for tiles of positions that every row sees
         const int free_lo = p.window > 0 ? len - p.window : 0, free_hi = len - p.q_len + 1;

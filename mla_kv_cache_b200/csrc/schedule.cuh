@@ -30,20 +30,22 @@ struct Piece {
     int slot;           // workspace slot of a partial piece: 0 or 1
 };
 
-__device__ __forceinline__ int tiles_of(int len, int tile) { return (len + tile - 1) / tile; }
+__host__ __device__ __forceinline__ int tiles_of(int len, int tile) { return (len + tile - 1) / tile; }
 
 __device__ __forceinline__ int clamp_len(int len, int T_max) {
     return len < 0 ? 0 : (len > T_max ? T_max : len);
 }
 
+// First of the `window` positions before `end`, not below 0 (compared before it is subtracted:
+// end may be negative and a window as large as an int).
+__host__ __device__ __forceinline__ int window_start(int end, int window) { return end > window ? end - window : 0; }
+
 // First cached position any query of a sequence of length len can see: 0, unless the
 // L newest tokens attend through a sliding window of `window` tokens (window > 0), in
 // which case the oldest of them, at position len - L, sees back to len - L + 1 - window.
 // The tiles of a sequence cover [active_start, len).
-__device__ __forceinline__ int active_start(int len, int q_len, int window) {
-    if (window <= 0) return 0;
-    const int s = len - q_len + 1 - window;
-    return s > 0 ? s : 0;
+__host__ __device__ __forceinline__ int active_start(int len, int q_len, int window) {
+    return window > 0 ? window_start(len - q_len + 1, window) : 0;
 }
 
 // Warp 0 of the block fills s_prefix[0..B] with the exclusive prefix of tiles per

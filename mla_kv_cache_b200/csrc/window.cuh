@@ -9,7 +9,7 @@
 
 namespace kvattn {
 
-__device__ __forceinline__ int active_start_on(int align, int len, int q_len, int window) {
+__host__ __device__ __forceinline__ int active_start_on(int align, int len, int q_len, int window) {
     const int s = active_start(len, q_len, window);
     return align > 1 ? s - s % align : s;
 }
