@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
         for (int v = 0; v < VEC; ++v) res[v] += s_acc[w][col + v] * f;
     }
     // a row may have no visible position in any partial (a new token before the cache's
-    // start): out 0, lse -inf
-    const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    // start): out 0, lse -inf; a NaN stays NaN in both
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         if constexpr (OUT16)
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(NW * 32) combine_kernel(const CombineParams p)
         else
             p.out[gh * D + col + v] = res[v] * inv;
     }
-    if (lane == 0) p.lse[gh] = tot > 0.f ? M + __logf(tot) : -INFINITY;
+    if (lane == 0) p.lse[gh] = tot == 0.f ? -INFINITY : M + __logf(tot);
 }
 
 }  // namespace kvattn
