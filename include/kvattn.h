@@ -424,10 +424,10 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
  * the unit's largest (11 significant bits); accumulation is fp32.
  * head_dim 128, n_q_heads / n_kv_heads <= 64, page_size a multiple of 128 (paged); batch *
  * q_len <= 4096.  A page outside the pool reads as rows of zeros.  Scales from 2^-60 to 2^60
- * keep full precision.  Codes and scales past a
- * sequence's length are never read into a result; everything else as for
- * kvattn_gqa_decode_fp8.  With q_len > 1 a new token's value scale has to be finite also for the
- * older new tokens, which give it weight zero.
+ * keep full precision.  Codes and scales past a sequence's length are never read into a result,
+ * and neither are those of positions that a query must not see (before its window; newer
+ * tokens than it): NaN there leaves its result alone.  Everything else as for
+ * kvattn_gqa_decode_fp8.
  */
 int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales,
                                const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, int num_pages,

@@ -590,7 +590,7 @@ int run_rs(const RsParams &base, const CUtensorMap &kmap, const CUtensorMap &vma
     }
     p.ws_lse = reinterpret_cast<float *>(ws);
     p.ws_o = reinterpret_cast<float *>(static_cast<char *>(ws) + lse_bytes);
-    auto kern = rs_decode_kernel<MT, NR>;
+    auto kern = (p.q_len > 1 || p.window > 0) ? rs_decode_kernel<MT, NR, true> : rs_decode_kernel<MT, NR, false>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kern), dev, smem);
     if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(row-scaled decode)");
     kern<<<p.workers, rs::NTHREADS, smem, stream>>>(p, kmap, vmap);

@@ -87,6 +87,8 @@ __device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t &a, uint32_t &b) {
         : "=r"(a), "=r"(b)
         : "r"(w));
 }
+// The NaN codes (0x7F or 0xFF) among four E4M3 codes: 0x80 in their bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -109,7 +111,8 @@ __device__ __forceinline__ Piece piece_on(const int *s_prefix, int B, int U, lon
 }  // namespace rs
 
 // NR: rows of an m-tile in use, 16 or (with one m-tile) 8, which halves a thread's rows.
-template <int MT, int NR>
+// MULTI: several new tokens or a window, so that a tile may hold tokens which a row must not see.
+template <int MT, int NR, bool MULTI>
 __global__ void __launch_bounds__(rs::NTHREADS, 1)
 rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using namespace rs;
@@ -377,6 +380,7 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
             }
             // ---- scales, mask, running maximum of s + log2(vs)
             const bool masked = y < tok0 || tok0 + TILE > free_hi || tok0 < free_lo;
+            uint32_t vis = 0xFFFFu;                // seen: bit 4 nt + e (element e of n-tile nt)
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
@@ -388,7 +392,10 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
                     float x = sc[nt][e] * (cs[h] * (e & 1 ? ks.y : ks.x));
                     if (masked) {
                         const int at = y + r0 + nt * 8 + 2 * c + (e & 1);
-                        if (!(at >= tok0 && at >= lo[h] && at < hi[h])) x = -INFINITY;
+                        if (!(at >= tok0 && at >= lo[h] && at < hi[h])) {
+                            x = -INFINITY;
+                            if (MULTI) vis &= ~(1u << (4 * nt + e));
+                        }
                     }
                     sc[nt][e] = x;
                     mx[h] = fmaxf(mx[h], x + (e & 1 ? lv.y : lv.x));
@@ -429,6 +436,42 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
                     pa[nt >> 1][2 * (nt & 1) + h] = pack_f16x2(a * vs.x, b * vs.y);
                 }
             }
+            // ---- a token that a row must not see takes no part in it, whatever its scale and codes are: a
+            //      weight of zero would still make NaN of them.  So the weights are cleared, and where the
+            //      block has NaN codes the product is taken of a copy without them and the elements they belong
+            //      to are found one by one.  (Without MULTI only a unit's last tile has such tokens, and the row
+            //      sees them in the tile before.)
+            uint32_t vp = vb;
+            bool nan_codes = false;
+            if (MULTI && masked) {
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        const uint32_t b = vis >> (4 * nt + 2 * h);
+                        pa[nt >> 1][2 * (nt & 1) + h] &= (b & 1 ? 0x0000FFFFu : 0u) | (b & 2 ? 0xFFFF0000u : 0u);
+                    }
+                const uint4 *src = reinterpret_cast<const uint4 *>(smem + s * STAGE + KV_BYTES + r0 * 128);
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = lane; i < BLK * 8; i += 32) {
+                    const uint4 w = src[i];
+                    any |= nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w);
+                }
+                nan_codes = __any_sync(0xffffffffu, any != 0);
+                if (nan_codes) {
+                    // (the warp's part of the join is free until the piece's end)
+                    uint4 *copy = reinterpret_cast<uint4 *>(my_merge);
+                    auto clean = [](uint32_t w) { return w & ~((nan_bytes(w) >> 7) * 0xFFu); };
+#pragma unroll 1
+                    for (int i = lane; i < BLK * 8; i += 32) {
+                        const uint4 w = src[i];
+                        copy[i] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+                    }
+                    __syncwarp();
+                    vp = smem_u32(my_merge) + (vb - (base + KV_BYTES));
+                }
+            }
             // ---- O += P V: the transposed load hands out pairs of dimensions (2p, 2p + 1) of two
             //      tokens; the even and the odd dimensions of a 16-byte chunk make an n-tile each
 #pragma unroll
@@ -436,7 +479,7 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
 #pragma unroll
                 for (int ch = 0; ch < D / 16; ch += 2) {
                     uint32_t w[4];
-                    ldmatrix_x4_trans((vb ^ (ch * 16)) + st * 2048, w[0], w[1], w[2], w[3]);
+                    ldmatrix_x4_trans((vp ^ (ch * 16)) + st * 2048, w[0], w[1], w[2], w[3]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         uint32_t b0, b1;
@@ -446,6 +489,33 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
                         mma_f16(o[2 * (ch + x) + 1], pa[st], b0, b1);
                     }
                 }
+            if (MULTI && nan_codes) {
+                // bit 4 ch + i of a row: a token that it sees has NaN at dimension 16 ch + 4 c + i
+                uint32_t bad[2] = {0u, 0u};
+#pragma unroll 1
+                for (int t = 0; t < BLK; ++t) {
+                    // (token 8 nt + 2 c' + i lies with lane c' of the row's four)
+                    const uint32_t of = __shfl_sync(0xffffffffu, vis, (lane & 28) | ((t >> 1) & 3));
+                    const uint8_t *row = smem + s * STAGE + KV_BYTES + (r0 + t) * 128 + 4 * c;
+                    uint32_t found = 0u;
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        const uint32_t n = nan_bytes(*reinterpret_cast<const uint32_t *>(row + ((ch ^ (t & 7)) << 4)));
+                        found |= ((n >> 7 & 1u) | (n >> 14 & 2u) | (n >> 21 & 4u) | (n >> 28 & 8u)) << (4 * ch);
+                    }
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        if (of >> (4 * (t >> 3) + 2 * h + (t & 1)) & 1u) bad[h] |= found;
+                }
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int ch = 0; ch < D / 16; ++ch)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)     // (the even dimensions' n-tile, then the odd ones')
+                            if (bad[h] >> (4 * ch + i) & 1u) o[2 * ch + (i & 1)][2 * h + (i >> 1)] = NAN;
+                __syncwarp();                           // (the copy is read)
+            }
             if (blk + NTS >= n_blk || (blk + NTS) / BPT != it) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->empty[s]);
@@ -507,8 +577,8 @@ rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, con
             for (int t = 0; t < NTS; ++t) {
                 const float w = wts[r * NTS + t];
                 const float4 x = *reinterpret_cast<const float4 *>(merge + (t * MT + rmt) * MERGE_FLOATS + rrow * MPAD + col);
-                // (a warp that saw nothing of this row adds nothing)
-                if (w != 0.f) { v.x += w * x.x; v.y += w * x.y; v.z += w * x.z; v.w += w * x.w; }
+                // (a warp that saw nothing of this row has zeros; a NaN stays under a weight that ran out of range)
+                v.x += w * x.x; v.y += w * x.y; v.z += w * x.z; v.w += w * x.w;
             }
             if (done.whole) {
                 const int qi = r / p.g;
