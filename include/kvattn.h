@@ -455,8 +455,8 @@ int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const 
  *              captured graphs) need a workspace each; the library allocates nothing.
  *   head_dim 64 or 128; (n_q_heads / n_kv_heads) * q_len <= 128; batch * q_len <= 4096;
  *   batch * n_kv_heads * max_seq_len and n_kv_heads * max_prefix_len < 2^31.
- * The softmax weights enter the value products as bf16; sums and outputs accumulate in fp32.
- * Rows at or past prefix_len and seq_lens[b] are never read into a result.  With q_len > 1 a
+ * The softmax weights enter the value products as bf16; sums and outputs accumulate in fp32,
+ * for cached values of up to 2^80 in size.  Rows at or past prefix_len and seq_lens[b] are never read into a result.  With q_len > 1 a
  * new token's cached value has to be finite also for the older new tokens, which give it
  * weight zero.
  *

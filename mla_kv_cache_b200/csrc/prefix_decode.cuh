@@ -108,7 +108,10 @@ constexpr int REGS_LAUNCH = 168, REGS_CTRL = 56, REGS_SOFT = 224;
 static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= NTHREADS * REGS_LAUNCH, "registers of the launch");
 constexpr int CHUNK = 128 * 128;          // [128 rows x 128 bytes]
 constexpr int NS_MAX = 10;
-constexpr float RESCALE = 8.f, LIMIT = 64.f;
+// How far (log2 units) scores may exceed the maximum the weights are taken against: RESCALE from the
+// next step on, LIMIT within a step.  Sums then stay below (2^8 T + 2^16 TILE) of the largest value over T
+// tokens, so values of up to 2^80 keep them in range (with a LIMIT of 64 values above 2^60 left it).
+constexpr float RESCALE = 8.f, LIMIT = 16.f;
 // Line positions (see above), and the least a worker takes.
 constexpr uint32_t WP2 = 8, WP1 = 6, WS = 6, UP2 = 4, UP1 = 1, US = 3, W_MIN = 8;
 constexpr long long LINE_LIMIT = 1ll << 30;
