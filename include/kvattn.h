@@ -387,7 +387,8 @@ int kvattn_mla_rope_append_fp8(uint16_t *q_rope, const uint16_t *latent_new, con
  *   head_dim   a multiple of 16, <= 256
  * The angle is formed in fp64 and the scales and codes from the fp32 rotated values.
  * n_tokens may be 0 (nothing is launched).  q_out, the pools and the scales must not overlap
- * each other or the inputs (but for q in place).
+ * each other or the inputs (but for q in place).  Rows of one stride that lie between each
+ * other, as q_out's between the keys and values of a fused projection, do not overlap.
  */
 int kvattn_rope_append_rowscale(const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new,
                                 const int32_t *positions, const int64_t *slots, uint16_t *q_out, uint8_t *k_pages,

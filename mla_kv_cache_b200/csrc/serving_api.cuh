@@ -15,6 +15,17 @@ size_t span(long long N, long long stride, long long row, int size) {
     return (size_t)((N - 1) * stride + row) * size;
 }
 
+// Whether N rows of `na` 2-byte elements, `sa` apart, share memory with N rows of `nb`, `sb` apart.  Rows of
+// one stride may lie between each other, as the slices of a fused projection do.
+bool rows_overlap(const void *a, long long sa, long long na, const void *b, long long sb, long long nb, long long N) {
+    if (!overlaps(a, span(N, sa, na, 2), b, span(N, sb, nb, 2))) return false;
+    if (sa != sb) return true;
+    // b's row from the start of the row of a at or before it
+    const long long diff = (long long)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2;
+    const long long at = (diff % sa + sa) % sa;
+    return at < na || at + nb > sa;
+}
+
 template <int D>
 int launch_prefix(PrefixParams &p, const CUtensorMap *maps, DeviceState *dev, cudaStream_t s) {
     using C = pfx::Cfg<D>;
@@ -209,13 +220,17 @@ int kvattn_rope_append_rowscale(const uint16_t *q, const uint16_t *k_new, const 
     const void *outs[5] = {k_pages, v_pages, k_scales, v_scales, q_out};
     const size_t on[5] = {pool * head_dim, pool * head_dim, pool * 4, pool * 4,
                           q ? span(n_tokens, q_out_stride, q_row, 2) : 0};
-    // (in place: the query's own rows, which may lie between the keys and values of a fused projection)
+    // the rotated queries may be written in place, and next to the keys and values of a fused projection
+    const long long stride[3] = {q_stride, k_stride, v_stride}, row[3] = {q_row, kv_row, kv_row};
     const bool in_place = q && q_out == q && q_out_stride == q_stride;
     for (int i = 0; i < 5; ++i) {
         if (!outs[i]) continue;
-        for (int k = 0; k < 5; ++k)
-            if (ins[k] && !(i == 4 && in_place && k < 3) && overlaps(outs[i], on[i], ins[k], in[k]))
+        for (int k = 0; k < 5; ++k) {
+            if (!ins[k] || (i == 4 && k == 0 && in_place)) continue;
+            if (i == 4 && k < 3 ? rows_overlap(q_out, q_out_stride, q_row, ins[k], stride[k], row[k], n_tokens)
+                                : overlaps(outs[i], on[i], ins[k], in[k]))
                 return KVATTN_ERR_INVALID_ARG;
+        }
         for (int k = i + 1; k < 5; ++k)
             if (outs[k] && overlaps(outs[i], on[i], outs[k], on[k])) return KVATTN_ERR_INVALID_ARG;
     }
