@@ -402,7 +402,9 @@ int kvattn_rope_append_rowscale(const uint16_t *q, const uint16_t *k_new, const 
  *   slots         device int64 [n_tokens]; a slot outside the pool gives a row of zeros
  *   k_out, v_out  device bf16 [n_kv_heads, n_tokens, head_dim], heads k_head_stride /
  *                 v_head_stride elements apart (a multiple of 8): the layout
- *                 kvattn_gqa_decode_prefix takes its prefix in, and a part of a longer one
+ *                 kvattn_gqa_decode_prefix takes its prefix in, and a part of a longer one; they
+ *                 must not overlap the inputs or each other (heads that alternate in one
+ *                 buffer do not)
  * head_dim a multiple of 16, <= 256.  n_tokens may be 0.
  */
 int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales, const float *v_scales,

@@ -307,7 +307,10 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
     const size_t kn = span(n_kv_heads, k_head_stride, row, 2), vn = span(n_kv_heads, v_head_stride, row, 2);
     for (int k = 0; k < 5; ++k)
         if (overlaps(k_out, kn, ins[k], in[k]) || overlaps(v_out, vn, ins[k], in[k])) return KVATTN_ERR_INVALID_ARG;
-    if (overlaps(k_out, kn, v_out, vn)) return KVATTN_ERR_INVALID_ARG;
+    // (the heads of the two may alternate in one buffer)
+    if (n_kv_heads > 1 ? rows_overlap(k_out, k_head_stride, row, v_out, v_head_stride, row, n_kv_heads)
+                       : overlaps(k_out, kn, v_out, vn))
+        return KVATTN_ERR_INVALID_ARG;
     DeviceState *dev = nullptr;
     st = device_state(&dev);
     if (st != KVATTN_OK) return st;

@@ -1,5 +1,5 @@
 """GPU tests of strided operands that lie between one another: rotated queries next to the keys and values of a fused
-projection (B200)."""
+projection, rows read back into alternating heads of one buffer (B200)."""
 import pytest
 import torch
 
@@ -41,3 +41,16 @@ def test_rotated_queries_into_the_projection():
     with pytest.raises(kb.KvattnError):          # one head too far: the last query head is the first key head
         dev = x.cuda()
         kb.kvattn_rope_append_rowscale(dev[:, :NQ], dev[:, NQ - 1:NQ - 1 + NKV], dev[:, NQ + NKV:NQ + 2 * NKV], pos, slots, *pools())
+
+
+@pytest.mark.parametrize("n_kv", [1, 2, 5])
+def test_read_back_into_alternating_heads(n_kv):
+    g = torch.Generator().manual_seed(n_kv)
+    codes = torch.randint(0, 0x70, (2, P, n_kv, S, D), generator=g).to(torch.uint8).cuda()
+    scales = torch.rand((2, P, n_kv, S), generator=g).cuda()
+    slots = torch.randperm(P * S, generator=g)[:N].cuda()
+    k, v = kb.kvattn_gather_rowscale(codes[0], codes[1], scales[0], scales[1], slots)
+    both = torch.full((n_kv, 2, N, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kb.kvattn_gather_rowscale(codes[0], codes[1], scales[0], scales[1], slots, k_out=both[:, 0], v_out=both[:, 1])
+    torch.cuda.synchronize()
+    assert torch.equal(both[:, 0], k) and torch.equal(both[:, 1], v)

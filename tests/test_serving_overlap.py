@@ -1,8 +1,8 @@
-"""Overlaps of strided operands on the CPU: queries rotated in place whose rows run into their keys or values are
-refused on the host (fake, never-dereferenced addresses)."""
+"""Overlaps of strided operands on the CPU: queries rotated in place whose rows run into their keys or values, and read
+back rows that run into each other, are refused on the host (fake, never-dereferenced addresses)."""
 import pytest
 
-from tests.test_serving_abi import A, APPEND, INVALID, call, lib  # noqa: F401
+from tests.test_serving_abi import A, APPEND, GATHER, INVALID, call, lib  # noqa: F401
 
 # a fused projection of 8 query heads, 2 of keys and 2 of values, 128 each: rows of 1536 elements
 FUSED = dict(q=A, q_out=A, k=A + 2 * 1024, v=A + 2 * 1280, qs=1536, qos=1536, kst=1536, vst=1536)
@@ -21,3 +21,13 @@ FUSED = dict(q=A, q_out=A, k=A + 2 * 1024, v=A + 2 * 1280, qs=1536, qos=1536, ks
 ], ids=range(9))
 def test_queries_that_run_into_their_keys_or_values(lib, kw):  # noqa: F811
     assert call(lib, "kvattn_rope_append_rowscale", APPEND, {**FUSED, **kw}) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(vo=6 * A + 2 * 12800, kh=25600, vh=25616),      # alternating heads of other strides
+    dict(vo=6 * A + 2 * 12792, kh=25600, vh=25600),      # a vector into the keys' row
+    dict(vo=6 * A + 2 * 12808, kh=25600, vh=25600),      # a vector into the next head's keys
+    dict(vo=6 * A, kh=25600, vh=25600),
+], ids=range(4))
+def test_read_back_rows_that_run_into_each_other(lib, kw):  # noqa: F811
+    assert call(lib, "kvattn_gather_rowscale", GATHER, kw) == INVALID
