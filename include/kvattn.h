@@ -509,8 +509,8 @@ int kvattn_gqa_decode_prefix_paged(const uint16_t *q, const uint16_t *k_pages, c
  *   tokens        device int32 [batch, n_drafts + 1]: the accepted drafts, the drawn token, -1
  * n_drafts may be 0 (then a plain draw from target_probs; draft_tokens and u_accept may be
  * NULL); n_drafts <= 1024, batch <= 4096, vocab <= 2^28.  Probabilities need not sum to one and
- * are not infinite; negative and NaN entries are never drawn; a row without a positive entry
- * gives token -1.
+ * are not infinite; target entries of zero or less and NaN are never accepted or drawn, draft
+ * entries below zero count as zero; a row without a positive entry gives token -1.
  * Rows whose strides and pointers are multiples of 16 bytes are read in vectors, others by
  * element.
  */

@@ -63,6 +63,26 @@ __device__ __forceinline__ void prob_unpack(const uint4 &w, float (&v)[8]) {
     for (int t = 0; t < 4; ++t) { v[2 * t] = bf16_lo(a[t]); v[2 * t + 1] = bf16_hi(a[t]); }
 }
 
+// Draft entries: those below zero count as zero, so that no target entry of zero or less is accepted or
+// drawn (NaN stays NaN).
+__device__ __forceinline__ float draft_f32(float x) {
+    float m;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(x));
+    return m;
+}
+__device__ __forceinline__ float draft_f32(__nv_bfloat16 x) { return draft_f32(__bfloat162float(x)); }
+__device__ __forceinline__ void draft_unpack(const uint4 &w, float (&v)[4]) {
+    prob_unpack(w, v);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = draft_f32(v[t]);
+}
+__device__ __forceinline__ void draft_unpack(const uint4 &w, float (&v)[8]) {
+    uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a[t]) : "r"(0u));
+    prob_unpack(make_uint4(a[0], a[1], a[2], a[3]), v);
+}
+
 // The row that is drawn from: r(v) = max(p(v) - q(v), 0), or max(p(v), 0) without q; a point
 // draft is a q of 1 at its token.  The comparison is exact in fp32 and false for NaN, so such an
 // entry is never drawn; the difference is taken in 64 bits.
@@ -75,7 +95,7 @@ struct ResidualRow {
         return pv > y ? (double)pv - (double)y : 0.0;
     }
     __device__ __forceinline__ double at(int v) const {
-        return value(prob_f32(p[v]), q != nullptr ? prob_f32(q[v]) : 0.f, v);
+        return value(prob_f32(p[v]), q != nullptr ? draft_f32(q[v]) : 0.f, v);
     }
 };
 
@@ -102,7 +122,7 @@ __device__ __forceinline__ double residual_sum(const ResidualRow<T> &r, int v0, 
             for (int u = 0; u < U; ++u) {
                 float x[N], y[N];
                 prob_unpack(a[u], x);
-                prob_unpack(b[u], y);
+                draft_unpack(b[u], y);
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
                     const int w = v + u * 32 * N + e;
@@ -122,7 +142,7 @@ __device__ __forceinline__ double residual_sum(const ResidualRow<T> &r, int v0, 
             for (int u = 0; u < U; ++u) {
                 const int w = v + 32 * u;
                 x[u] = w < v1 ? prob_f32(r.p[w]) : 0.f;
-                y[u] = w < v1 && r.q != nullptr ? prob_f32(r.q[w]) : 0.f;
+                y[u] = w < v1 && r.q != nullptr ? draft_f32(r.q[w]) : 0.f;
             }
 #pragma unroll
             for (int u = 0; u < U; u += 2) {
@@ -173,12 +193,12 @@ __device__ __forceinline__ int residual_find(const ResidualRow<T> &r, int v0, in
             uint4 c = make_uint4(0u, 0u, 0u, 0u);
             if (r.q != nullptr) c = __ldg(reinterpret_cast<const uint4 *>(r.q + w0));
             prob_unpack(a, x);
-            prob_unpack(c, y);
+            draft_unpack(c, y);
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 x[e] = w0 + e < v1 ? prob_f32(r.p[w0 + e]) : 0.f;
-                y[e] = w0 + e < v1 && r.q != nullptr ? prob_f32(r.q[w0 + e]) : 0.f;
+                y[e] = w0 + e < v1 && r.q != nullptr ? draft_f32(r.q[w0 + e]) : 0.f;
             }
         }
         double mine = 0.0;
@@ -259,7 +279,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(co
             bool refuse = i < len;                // also for a token outside the vocabulary, and for NaN
             if (i < len && x >= 0 && x < a.V) {
                 const double px = (double)prob_f32(p[(long long)i * a.p_l + x]);
-                const double qx = q != nullptr ? (double)prob_f32(q[(long long)i * a.q_l + x]) : 1.0;
+                const double qx = q != nullptr ? (double)draft_f32(q[(long long)i * a.q_l + x]) : 1.0;
                 refuse = !((double)u * qx < px);
             }
             const unsigned m = __ballot_sync(0xffffffffu, refuse);
