@@ -150,6 +150,11 @@ def _stream_handle(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _window(window):
+    """A window as the C functions take it: one past 32 bits is longer than any cache."""
+    return min(int(window), 2 ** 31 - 1)
+
+
 def _check(t, name, dtype, shape=None):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -431,7 +436,7 @@ def kvattn_gqa_decode_fp8(q, k_cache, v_cache, seq_lens, scale, k_scale, v_scale
     _check(lse, "lse", torch.float32, shape_l)
     st = lib().kvattn_gqa_decode_fp8(q4.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(),
                                      T, B, L, n_q, n_kv, d, float(scale), float(k_scale), float(v_scale),
-                                     int(window), out.data_ptr(), lse.data_ptr(), _stream_handle(stream))
+                                     _window(window), out.data_ptr(), lse.data_ptr(), _stream_handle(stream))
     if st != KVATTN_OK:
         raise KvattnError(st, "kvattn_gqa_decode_fp8")
     return out, lse
@@ -629,7 +634,7 @@ def kvattn_gqa_decode_multi(q, k_cache, v_cache, seq_lens, scale, window=0, out=
     _check(out, "out", torch.float32, (B, L, n_q, d))
     _check(lse, "lse", torch.float32, (B, L, n_q))
     st = lib().kvattn_gqa_decode_multi(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(),
-                                       T, B, L, n_q, n_kv, d, float(scale), int(window), out.data_ptr(),
+                                       T, B, L, n_q, n_kv, d, float(scale), _window(window), out.data_ptr(),
                                        lse.data_ptr(), _stream_handle(stream))
     if st != KVATTN_OK:
         raise KvattnError(st, "kvattn_gqa_decode_multi")
@@ -651,6 +656,8 @@ def _elsewhere(t, stream):
     stream is given.  Otherwise the contexts under which it can: what the call allocates then
     belongs to that stream."""
     import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
     index = t.get_device()
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
@@ -663,18 +670,26 @@ def _elsewhere(t, stream):
 
 def _at(t, name, dtype, shape, index):
     """Address of a dense tensor of this type and shape on device `index`."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass                               # (no tensor, as is said next)
     _check(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def _codes_at(t, name, shape, index):
     """Address of E4M3 codes (float8_e4m3fn or uint8)."""
-    if t.shape == shape and t.element_size() == 1 and t.get_device() == index and t.is_contiguous():
-        import torch
-        if t.dtype in (torch.float8_e4m3fn, torch.uint8):
+    import torch
+    try:
+        if t.shape == shape and t.element_size() == 1 and t.get_device() == index and t.is_contiguous() and \
+                t.dtype in (torch.float8_e4m3fn, torch.uint8):
             return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     _check_e4m3(t, name, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
@@ -732,7 +747,7 @@ def kvattn_rope_append_rowscale(q, k_new, v_new, positions, slots, k_pages, v_pa
     args = (qa or None, kn, vn, pos, _at(slots, "slots", torch.int64, (N,), ix), qo or None,
             _codes_at(k_pages, "k_pages", pages, ix), _codes_at(v_pages, "v_pages", pages, ix),
             _at(k_scales, "k_scales", f32, rows, ix), _at(v_scales, "v_scales", f32, rows, ix), N, n_q, n_kv, d, qs, qos,
-            ks, vs, P, S, rope_base, 1 if interleaved else 0, _raw_stream(ix))
+            ks, vs, P, S, float(rope_base), 1 if interleaved else 0, _raw_stream(ix))
     if N == 0:
         return q_out
     rc = lib().kvattn_rope_append_rowscale(*args)
@@ -821,7 +836,7 @@ def kvattn_gqa_decode_rowscale(q, k_pages, v_pages, k_scales, v_scales, seq_lens
         _at(q, "q", torch.bfloat16, q.shape, ix), _codes_at(k_pages, "k_pages", pages, ix),
         _codes_at(v_pages, "v_pages", pages, ix), _at(k_scales, "k_scales", f32, rows, ix),
         _at(v_scales, "v_scales", f32, rows, ix), table, _at(seq_lens, "seq_lens", i32, (B,), ix), P, S, M, B, L, n_q, n_kv,
-        d, scale, window, oa, la, _raw_stream(ix))
+        d, float(scale), _window(window), oa, la, _raw_stream(ix))
     if rc != KVATTN_OK:
         raise KvattnError(rc, "kvattn_gqa_decode_rowscale")
     return out, lse
@@ -871,7 +886,7 @@ def kvattn_gqa_decode_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache
     args = (_at(q, "q", bf16, q.shape, ix), _at(k_prefix, "k_prefix", bf16, prefix, ix),
             _at(v_prefix, "v_prefix", bf16, prefix, ix), _at(prefix_len, "prefix_len", i32, (1,), ix), P,
             _at(k_cache, "k_cache", bf16, own, ix), _at(v_cache, "v_cache", bf16, own, ix),
-            _at(seq_lens, "seq_lens", i32, (B,), ix), T, B, L, n_q, n_kv, d, scale)
+            _at(seq_lens, "seq_lens", i32, (B,), ix), T, B, L, n_q, n_kv, d, float(scale))
     out, lse, oa, la = _outputs(q, out, lse, ix)
     ws, size = _workspace(workspace, q, ix, P, T, B, L, n_q, n_kv, d)
     rc = lib().kvattn_gqa_decode_prefix(*args, oa, la, ws.data_ptr(), size, _raw_stream(ix))
@@ -900,7 +915,7 @@ def kvattn_gqa_decode_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len
     args = (_at(q, "q", bf16, q.shape, ix), _at(k_pages, "k_pages", bf16, pages, ix),
             _at(v_pages, "v_pages", bf16, pages, ix), _at(prefix_table, "prefix_table", i32, (PM,), ix),
             _at(prefix_len, "prefix_len", i32, (1,), ix), PM, _at(block_table, "block_table", i32, (B, M), ix),
-            _at(seq_lens, "seq_lens", i32, (B,), ix), N, S, M, B, L, n_q, n_kv, d, scale)
+            _at(seq_lens, "seq_lens", i32, (B,), ix), N, S, M, B, L, n_q, n_kv, d, float(scale))
     out, lse, oa, la = _outputs(q, out, lse, ix)
     ws, size = _workspace(workspace, q, ix, PM * S, M * S, B, L, n_q, n_kv, d)
     rc = lib().kvattn_gqa_decode_prefix_paged(*args, oa, la, ws.data_ptr(), size, _raw_stream(ix))
