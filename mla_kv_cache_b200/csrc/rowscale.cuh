@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kRowThreads) row_append_kernel(const __grid_co
     // Of these in flight: two of the queries (8192 tokens of 64 + 2 * 8 heads of 128: 57.3 us, 58.5 with
     // one), one of the keys or values (two cost registers: 17.3 us for 8192 tokens of 8 + 2 * 8 heads of 64,
     // 14.3 with one, against 7.4 and 8.5 for 700 of the former).
-    constexpr int UQ = 2, U = 1;
+    constexpr int UQ = 2;
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int n = (int)(item / p.parts), part = (int)(item - (long long)n * p.parts);
@@ -176,34 +176,27 @@ __global__ void __launch_bounds__(kRowThreads) row_append_kernel(const __grid_co
         const __nv_bfloat16 *src = kv ? p.v_new + (long long)n * p.v_stride : p.k_new + (long long)n * p.k_stride;
         uint8_t *codes = kv ? p.v_pages : p.k_pages;
         float *scales = kv ? p.v_scales : p.k_scales;
-        for (int base = j0; base < j1; base += RPW * U) {
-            RowHalves x[U];
+        for (int base = j0; base < j1; base += RPW) {
+            const int j = base + sub;
+            RowHalves x;
+            x.lo = x.hi = make_uint4(0u, 0u, 0u, 0u);
+            if (j < j1 && lane_on) x = load(src + j * p.d);
+            float a[8], b[8];
+            unpack8(x.lo, a);
+            unpack8(x.hi, b);
+            if (p.rotate && kv == 0 && lane_on) turn(a, b);
+            float m = 0.f;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = base + u * RPW + sub;
-                x[u].lo = x[u].hi = make_uint4(0u, 0u, 0u, 0u);
-                if (j < j1 && lane_on) x[u] = load(src + j * p.d);
-            }
+            for (int t = 0; t < 8; ++t) m = fmaxf(m, fmaxf(fabsf(a[t]), fabsf(b[t])));     // (passes over NaN)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = base + u * RPW + sub;
-                float a[8], b[8];
-                unpack8(x[u].lo, a);
-                unpack8(x[u].hi, b);
-                if (p.rotate && kv == 0 && lane_on) turn(a, b);
-                float m = 0.f;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) m = fmaxf(m, fmaxf(fabsf(a[t]), fabsf(b[t])));     // (passes over NaN)
-#pragma unroll
-                for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (j >= j1 || !lane_on) continue;
-                m = fminf(fmaxf(m, kRowAmaxMin), kRowAmaxMax);
-                const float inv = __fdiv_rn(448.f, m);
-                const long long row = row0 + (long long)j * p.page_size;
-                *reinterpret_cast<uint2 *>(codes + row * p.d + at) = codes8(a, inv);
-                *reinterpret_cast<uint2 *>(codes + row * p.d + half + at) = codes8(b, inv);
-                if (l == 0) scales[row] = __fdiv_rn(m, 448.f);
-            }
+            for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (j >= j1 || !lane_on) continue;
+            m = fminf(fmaxf(m, kRowAmaxMin), kRowAmaxMax);
+            const float inv = __fdiv_rn(448.f, m);
+            const long long row = row0 + (long long)j * p.page_size;
+            *reinterpret_cast<uint2 *>(codes + row * p.d + at) = codes8(a, inv);
+            *reinterpret_cast<uint2 *>(codes + row * p.d + half + at) = codes8(b, inv);
+            if (l == 0) scales[row] = __fdiv_rn(m, 448.f);
         }
     }
 }
@@ -221,62 +214,42 @@ struct RowGatherParams {
 
 // Sixteen codes a lane (one 16-byte load, two 16-byte stores); LPR lanes make a row.  A CTA
 // takes consecutive tokens of one head, whose rows lie next to each other within a page.
-// Bound by memory (1 byte read and 2 written per element).
-constexpr int kGatherRows = 1;     // rows a lane has in flight (with 2 a prompt of 32768 tokens took 41.7 us, with 4 46.2; 39.7)
+// Bound by memory (1 byte read and 2 written per element).  A lane has one row of keys and one of
+// values in flight (with two a prompt of 32768 tokens took 41.7 us, with four 46.2; 39.7 so).
 template <int LPR>
 __global__ void __launch_bounds__(256) row_gather_kernel(const RowGatherParams p) {
-    constexpr int RPC = 256 / LPR;
-    constexpr int U = kGatherRows;
     const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int j = blockIdx.y;
-    if (l * 16 >= p.d) return;
-    long long row[U];
-    uint4 code[2 * U];
-    float sc[2 * U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const long long n = (long long)blockIdx.x * (RPC * U) + u * RPC + sub;
-        row[u] = -1;
-        if (n < p.N) {
-            const long long slot = __ldg(p.slots + n);
-            if (slot >= 0 && slot < p.n_slots) {
-                const long long page = slot / p.page_size;
-                row[u] = (page * p.n_kv + j) * p.page_size + (slot - page * p.page_size);
-            }
-        }
+    const long long n = (long long)blockIdx.x * (256 / LPR) + sub;
+    if (l * 16 >= p.d || n >= p.N) return;
+    uint4 code[2];
+    float sc[2] = {0.f, 0.f};
+    code[0] = code[1] = make_uint4(0u, 0u, 0u, 0u);
+    const long long slot = __ldg(p.slots + n);
+    if (slot >= 0 && slot < p.n_slots) {
+        const long long page = slot / p.page_size;
+        const long long row = (page * p.n_kv + j) * p.page_size + (slot - page * p.page_size);
+        code[0] = __ldcs(reinterpret_cast<const uint4 *>(p.k_pages + row * p.d + l * 16));
+        code[1] = __ldcs(reinterpret_cast<const uint4 *>(p.v_pages + row * p.d + l * 16));
+        sc[0] = __ldg(p.k_scales + row);
+        sc[1] = __ldg(p.v_scales + row);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        code[2 * u] = code[2 * u + 1] = make_uint4(0u, 0u, 0u, 0u);
-        sc[2 * u] = sc[2 * u + 1] = 0.f;
-        if (row[u] >= 0) {
-            code[2 * u] = __ldcs(reinterpret_cast<const uint4 *>(p.k_pages + row[u] * p.d + l * 16));
-            code[2 * u + 1] = __ldcs(reinterpret_cast<const uint4 *>(p.v_pages + row[u] * p.d + l * 16));
-            sc[2 * u] = __ldg(p.k_scales + row[u]);
-            sc[2 * u + 1] = __ldg(p.v_scales + row[u]);
+    for (int t = 0; t < 2; ++t) {
+        const uint32_t w[4] = {code[t].x, code[t].y, code[t].z, code[t].w};
+        const float s = sc[t];
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // (codes are exact in f16, so the product with the scale is rounded once to bf16)
+            const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[e] & 0xffffu), __NV_E4M3)));
+            const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[e] >> 16), __NV_E4M3)));
+            o[2 * e] = pack_bf16x2(a.x * s, a.y * s);
+            o[2 * e + 1] = pack_bf16x2(b.x * s, b.y * s);
         }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const long long n = (long long)blockIdx.x * (RPC * U) + u * RPC + sub;
-        if (n >= p.N) continue;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t w[4] = {code[2 * u + t].x, code[2 * u + t].y, code[2 * u + t].z, code[2 * u + t].w};
-            const float s = sc[2 * u + t];
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // (codes are exact in f16, so the product with the scale is rounded once to bf16)
-                const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[e] & 0xffffu), __NV_E4M3)));
-                const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[e] >> 16), __NV_E4M3)));
-                o[2 * e] = pack_bf16x2(a.x * s, a.y * s);
-                o[2 * e + 1] = pack_bf16x2(b.x * s, b.y * s);
-            }
-            uint4 *dst = reinterpret_cast<uint4 *>((t ? p.v_out + j * p.v_head : p.k_out + j * p.k_head) + n * p.d + l * 16);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        }
+        uint4 *dst = reinterpret_cast<uint4 *>((t ? p.v_out + j * p.v_head : p.k_out + j * p.k_head) + n * p.d + l * 16);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 

@@ -330,7 +330,7 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
     p.page_size = page_size;
     p.n_slots = (long long)num_pages * page_size;
     const int lpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
-    const int per = (256 / lpr) * kGatherRows;
+    const int per = 256 / lpr;
     const dim3 grid((unsigned)((n_tokens + per - 1) / per), (unsigned)n_kv_heads, 1);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (lpr == 4)
