@@ -51,7 +51,9 @@
  *    call may be replayed any number of times: its kernels derive the work split from
  *    the device-side seq_lens at every launch, so the lengths (not the shapes or
  *    pointers) may change between replays.  Calls that share a device must be ordered
- *    (same stream, or synchronised): they share the workspace.
+ *    (same stream, or synchronised): they share the workspace.  So must the row-scaled
+ *    decode's.  The appends, kvattn_gather_rowscale and kvattn_verify_drafts use no
+ *    workspace and the prefix decode the caller's, so that they may run beside other calls.
  *  - Thread safety: entry points may be called from several host threads; the
  *    workspace is guarded by a mutex, but see the ordering rule above.
  */
@@ -140,8 +142,10 @@ int kvattn_mla_decode(const uint16_t *q_latent, const uint16_t *q_rope,
  *             otherwise to all t <= p.  Tiles wholly before the earliest visible position
  *             are not read.
  *   out       device fp32 [batch, q_len, n_q_heads, head_dim];  lse fp32 [batch, q_len, n_q_heads]
- * A query with no visible position (p < 0) gets out = 0 and lse = -inf.  q_len == 1 and
- * window == 0 is exactly kvattn_gqa_decode.  head_dim 64 or 128; a window needs head_dim
+ * A query with no visible position (p < 0) gets out = 0 and lse = -inf.  Cached values of the
+ * newest q_len tokens have to be finite for all of them, and with a window so do those from
+ * the 128 positions before the earliest visible one on: a weight of zero does not hide NaN.
+ * q_len == 1 and window == 0 is exactly kvattn_gqa_decode.  head_dim 64 or 128; a window needs head_dim
  * 128 and n_q_heads / n_kv_heads <= 64; batch * q_len <= 4096 (KVATTN_ERR_UNSUPPORTED
  * otherwise).  With head_dim 128 and (n_q_heads / n_kv_heads) * q_len <= 64 one kernel
  * scores a group's heads at all q_len positions against each cache tile; otherwise the
@@ -440,7 +444,8 @@ int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const 
 /*
  * Decode for a batch whose sequences share a prefix: every new token attends to the same
  * prefix tokens and then, causally, to its own sequence's cache.  The prefix is read once for
- * the whole batch (a matrix product of all sequences' query rows), not once per sequence.
+ * every 256 query rows of a KV head (all sequences' rows make one matrix product with it), not
+ * once per sequence.
  *   q          device bf16 [batch, q_len, n_q_heads, head_dim], the newest tokens, oldest first
  *   k_prefix, v_prefix  device bf16 [n_kv_heads, max_prefix_len, head_dim]
  *   prefix_len device int32 [1], 0..max_prefix_len (clamped): tokens of the shared prefix
@@ -457,11 +462,13 @@ int kvattn_gqa_decode_rowscale(const uint16_t *q, const uint8_t *k_pages, const 
  *              call, never kept.  Calls that may run at the same time (other streams, other
  *              captured graphs) need a workspace each; the library allocates nothing.
  *   head_dim 64 or 128; (n_q_heads / n_kv_heads) * q_len <= 128; batch * q_len <= 4096;
- *   batch * n_kv_heads * max_seq_len and n_kv_heads * max_prefix_len < 2^31.
- * The softmax weights enter the value products as bf16; sums and outputs accumulate in fp32,
- * for cached values of up to 2^80 in size.  Rows at or past prefix_len and seq_lens[b] are never read into a result.  With q_len > 1 a
- * new token's cached value has to be finite also for the older new tokens, which give it
- * weight zero.
+ *   batch * n_kv_heads * max_seq_len and n_kv_heads * max_prefix_len < 2^31, and fewer than
+ *   about 2^27 tiles of 128 tokens in all, the prefix's counted for every 256 rows.
+ * The softmax weights enter the value products as bf16 (8 significant bits; kvattn_gqa_decode
+ * keeps about 16 of them in two parts); sums and outputs accumulate in fp32, for cached values
+ * of up to 2^80 in size.  Rows at or past prefix_len and seq_lens[b] are never read into a
+ * result.  With q_len > 1 a new token's cached value has to be finite also for the older new
+ * tokens, which give it weight zero.
  *
  * kvattn_gqa_decode_prefix_paged takes prefix and own tokens from one page pool:
  *   k_pages, v_pages  device bf16 [num_pages, n_kv_heads, page_size, head_dim], page_size a

@@ -16,8 +16,8 @@
 // each m-tile (measured, 8.7 cycles an MMA and scheduler), the conversions E4M3 -> f16 270.  Streaming
 // runs at 5.2 TB/s (16 equal sequences of 8192 tokens, 64 / 8 heads).  The same decode on tcgen05 with
 // E4M3 operands (query and weights in two E4M3 parts, the tokens on the MMA rows, whose maxima cross
-// the 128 token lanes) ran at 4.9; 42.4 us against 36.2 here for 16 sequences of 1024..8192 tokens, 20.4
-// against 14.4 for 8 of up to 1000 with 5 new tokens, 22.5 against 24.4 for 4 of 32768 with 32 / 1
+// the 128 token lanes) ran at 4.9; 42.4 us against 35.9 here for 16 sequences of 1024..8192 tokens, 20.4
+// against 15.1 for 8 of up to 1000 with 5 new tokens, 22.5 against 24.3 for 4 of 32768 with 32 / 1
 // heads.  The 8-bit mma.sync is no help: 20 cycles each here.
 //
 // Warps: a producer and 8 consumers.  A consumer works on 32 tokens at a time, all 128
@@ -111,7 +111,9 @@ __device__ __forceinline__ Piece piece_on(const int *s_prefix, int B, int U, lon
 }  // namespace rs
 
 // NR: rows of an m-tile in use, 16 or (with one m-tile) 8, which halves a thread's rows.
-// MULTI: several new tokens or a window, so that a tile may hold tokens which a row must not see.
+// MULTI: several new tokens or a window, so that a tile may hold tokens which a row must not see.  Their NaN
+// is kept out (below), for 16 ragged sequences with a window of 4096 at 31.3 us instead of 30.4, 8 of up to
+// 1000 with 5 new tokens at 15.1 instead of 14.4; one new token without a window pays nothing.
 template <int MT, int NR, bool MULTI>
 __global__ void __launch_bounds__(rs::NTHREADS, 1)
 rs_decode_kernel(const RsParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
