@@ -430,7 +430,7 @@ int kvattn_gather_rowscale(const uint8_t *k_pages, const uint8_t *v_pages, const
  * times a power of two), the softmax weights times their token's value scale in f16 relative to
  * the unit's largest (11 significant bits); accumulation is fp32.
  * head_dim 128, n_q_heads / n_kv_heads <= 64, page_size a multiple of 128 (paged); batch *
- * q_len <= 4096.  A page outside the pool reads as rows of zeros.  Scales from 2^-60 to 2^60
+ * q_len <= 4096.  A page outside the pool reads as rows of zeros.  Scales from 2^-40 to 2^40
  * keep full precision.  Codes and scales past a sequence's length are never read into a result,
  * and neither are those of positions that a query must not see (before its window; newer
  * tokens than it): NaN there leaves its result alone.  Everything else as for
