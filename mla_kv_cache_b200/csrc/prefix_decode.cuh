@@ -65,7 +65,7 @@
 // What bounds it now is the softmax warps: two a scheduler, each 1300-1500 cycles for 64 columns
 // when both run (the exponential unit's share is 1024), and 250-400 at each of four hand-overs.
 // Asking for the barriers' phases ahead of their use changed nothing.  A suffix is bound by
-// memory where it is long (4.2 TB/s at 8 sequences of up to 8000 tokens behind 32768) and by the
+// memory where it is long (4.5 TB/s at 8 sequences of up to 8000 tokens behind 32768) and by the
 // start and end of a piece, some 5000 cycles, where it is short.
 // Weights enter the value product rounded to bf16 (at most half a step, 2^-8 relative, each independent
 // of the others; the output is rounded to bf16 itself); sums, maxima and O are fp32.  A bf16 remainder
