@@ -624,6 +624,9 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
         const int r = lrow - (!pc.prefix && x == 1 ? suffix_shift(rows) : 0);
         const int q_on = r - lane;                    // the warp's first row
         const bool warp_on = q_on >= 0 && q_on < rows;
+        // (lanes past the rows hold scores of what else lies in the Q tile, NaN among it, and have no say in the
+        // rescaling: with it groups of 12 heads took 141 us where they take 129, of 7 37.9 and 35.4)
+        const bool on = r < rows;
         // the suffixes come last and all have as many rows: warps without any are done, and the
         // first answers for them
         if (!pc.prefix && !warp_on) return;
@@ -658,7 +661,7 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
             __syncwarp();
             if (lane == 0) mbar_arrive_n(&bars->sfree[buf], arrivals);
             if (warp_on) {
-                if (__any_sync(0xffffffffu, m_next != m)) {
+                if (__any_sync(0xffffffffu, on && m_next != m)) {
                     if (!settle()) return;
                     const float a = m == -INFINITY ? 1.f : fast_exp2(m - m_next);
                     l *= a;
@@ -681,7 +684,7 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
                 if (i == first) m = m_next = max128(s) * cs;
                 float lsum = weights64(s, cs, m, w);
                 const float tm = max128(s) * cs;
-                if (__any_sync(0xffffffffu, tm > m + LIMIT)) {
+                if (__any_sync(0xffffffffu, on && tm > m + LIMIT)) {
                     const float m_new = fmaxf(m, tm);
                     if (i != first) {
                         if (!settle()) return;
@@ -719,7 +722,6 @@ __device__ __forceinline__ void softmax_group(const PrefixParams &p, const Ctx &
             tc_fence_after();
         }
         if (warp_on) {
-            const bool on = r < rows;
             // (a NaN sum stays NaN)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
