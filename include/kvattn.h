@@ -46,14 +46,16 @@
  *  - Functions never throw or abort; they return a kvattn_status.
  *  - Scratch memory: the library keeps one workspace per device, grown with
  *    cudaMalloc when a call needs more than it holds and kept until
- *    kvattn_release_workspace().  A call that grows it is not capturable in a CUDA
+ *    kvattn_release_workspace(), and the outgrown ones too: captured graphs may use
+ *    them.  A call that grows it is not capturable in a CUDA
  *    graph; issue one call of the largest shape before capturing.  A captured decode
  *    call may be replayed any number of times: its kernels derive the work split from
  *    the device-side seq_lens at every launch, so the lengths (not the shapes or
  *    pointers) may change between replays.  Calls that share a device must be ordered
- *    (same stream, or synchronised): they share the workspace.  So must the row-scaled
- *    decode's.  The appends, kvattn_gather_rowscale and kvattn_verify_drafts use no
- *    workspace and the prefix decode the caller's, so that they may run beside other calls.
+ *    (same stream, or synchronised): they share the workspace.  That holds for the
+ *    row-scaled decode too; the appends, kvattn_gather_rowscale and kvattn_verify_drafts
+ *    use no workspace and the prefix decode the caller's, so that they may run beside
+ *    other calls.
  *  - Thread safety: entry points may be called from several host threads; the
  *    workspace is guarded by a mutex, but see the ordering rule above.
  */
@@ -535,7 +537,8 @@ const char *kvattn_last_error_detail(void);
 /* KVATTN_VERSION of the loaded library. */
 int kvattn_version(void);
 
-/* Frees the workspace of every device (waits for that device to be idle first). */
+/* Frees the workspace of every device (waits for that device to be idle first).  Graphs that
+ * captured calls are not to be replayed afterwards. */
 void kvattn_release_workspace(void);
 
 /*

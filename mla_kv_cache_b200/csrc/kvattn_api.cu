@@ -43,6 +43,8 @@ struct DeviceState {
     size_t ws_bytes = 0;
     void *aux = nullptr;          // the virtual batch of a multi-token call (lengths, block table)
     size_t aux_bytes = 0;
+    void *retired[64] = {};       // outgrown buffers
+    int n_retired = 0;
     struct Func {
         const void *kern;
         int smem;
@@ -78,27 +80,33 @@ int device_state(DeviceState **out) {
     return KVATTN_OK;
 }
 
-// Grows the calling device's workspace to at least `bytes` (caller holds g_mutex).
-int ensure_workspace(DeviceState *s, size_t bytes, void **ws) {
-    if (s->ws_bytes < bytes) {
-        if (s->ws) {
-            cudaError_t e = cudaDeviceSynchronize();
-            if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceSynchronize (workspace grow)");
-            cudaFree(s->ws);
-            s->ws = nullptr;
-            s->ws_bytes = 0;
-        }
-        size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
-        cudaError_t e = cudaMalloc(&s->ws, want);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            snprintf(t_detail, sizeof(t_detail), "cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
-            return KVATTN_ERR_NO_MEMORY;
-        }
-        s->ws_bytes = want;
+// Grows one of the calling device's buffers to at least `bytes` (caller holds g_mutex).  A captured graph
+// may still use the one before, so it is kept until kvattn_release_workspace; each at least doubles, so
+// that what is kept is no more than the last, and a few dozen hold all of a GPU's memory.
+int grow(DeviceState *s, void **buf, size_t *held, size_t bytes) {
+    if (*held >= bytes) return KVATTN_OK;
+    if (s->n_retired == (int)(sizeof(s->retired) / sizeof(s->retired[0]))) {
+        snprintf(t_detail, sizeof(t_detail), "workspace grown %d times", s->n_retired);
+        return KVATTN_ERR_NO_MEMORY;
     }
-    *ws = s->ws;
+    size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
+    if (want < 2 * *held) want = 2 * *held;
+    void *fresh = nullptr;
+    cudaError_t e = cudaMalloc(&fresh, want);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        snprintf(t_detail, sizeof(t_detail), "cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
+        return KVATTN_ERR_NO_MEMORY;
+    }
+    if (*buf) s->retired[s->n_retired++] = *buf;
+    *buf = fresh;
+    *held = want;
     return KVATTN_OK;
+}
+int ensure_workspace(DeviceState *s, size_t bytes, void **ws) {
+    const int st = grow(s, &s->ws, &s->ws_bytes, bytes);
+    if (st == KVATTN_OK) *ws = s->ws;
+    return st;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -683,22 +691,8 @@ int virtual_batch(DeviceState *dev, const int32_t *seq_lens, const int32_t *bloc
     const size_t need = lens_bytes + (size_t)B * L * mp * 4;
     {
         std::lock_guard<std::mutex> lk(g_mutex);
-        if (dev->aux_bytes < need) {
-            if (dev->aux) {
-                cudaError_t e = cudaDeviceSynchronize();
-                if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceSynchronize (aux grow)");
-                cudaFree(dev->aux);
-                dev->aux = nullptr;
-                dev->aux_bytes = 0;
-            }
-            cudaError_t e = cudaMalloc(&dev->aux, need);
-            if (e != cudaSuccess) {
-                cudaGetLastError();
-                snprintf(t_detail, sizeof(t_detail), "cudaMalloc(%zu): %s", need, cudaGetErrorString(e));
-                return KVATTN_ERR_NO_MEMORY;
-            }
-            dev->aux_bytes = need;
-        }
+        const int st = grow(dev, &dev->aux, &dev->aux_bytes, need);
+        if (st != KVATTN_OK) return st;
     }
     *vlens = static_cast<int32_t *>(dev->aux);
     *vtable = reinterpret_cast<int32_t *>(static_cast<char *>(dev->aux) + lens_bytes);
@@ -1363,20 +1357,16 @@ void kvattn_release_workspace(void) {
     int cur = 0;
     if (cudaGetDevice(&cur) != cudaSuccess) return;
     for (int d = 0; d < kMaxDevices; ++d) {
-        if (g_dev[d].ws) {
-            cudaSetDevice(d);
-            cudaDeviceSynchronize();
-            cudaFree(g_dev[d].ws);
-            g_dev[d].ws = nullptr;
-            g_dev[d].ws_bytes = 0;
-        }
-        if (g_dev[d].aux) {
-            cudaSetDevice(d);
-            cudaDeviceSynchronize();
-            cudaFree(g_dev[d].aux);
-            g_dev[d].aux = nullptr;
-            g_dev[d].aux_bytes = 0;
-        }
+        DeviceState &s = g_dev[d];
+        if (!s.ws && !s.aux) continue;
+        cudaSetDevice(d);
+        cudaDeviceSynchronize();
+        for (int i = 0; i < s.n_retired; ++i) cudaFree(s.retired[i]);
+        if (s.ws) cudaFree(s.ws);
+        if (s.aux) cudaFree(s.aux);
+        s.n_retired = 0;
+        s.ws = s.aux = nullptr;
+        s.ws_bytes = s.aux_bytes = 0;
     }
     cudaSetDevice(cur);
 }
